@@ -99,7 +99,8 @@ typedef enum awq_status {
   AWQ_ERR_CUDA = 6,        /* a CUDA runtime call or kernel launch failed */
   AWQ_ERR_TIMEOUT = 7,     /* device side: a bounded pipeline wait expired */
   AWQ_ERR_NONFINITE = 8,   /* device side: awq_pack met an inf or NaN weight */
-  AWQ_ERR_BOUNDS = 9       /* device side, debug build only: an index check failed (the access was skipped) */
+  AWQ_ERR_BOUNDS = 9       /* device side: a bad block number, row start or length of a key/value cache batch, or, in
+                              the debug build, a failed index check (the access was skipped) */
 } awq_status;
 
 typedef struct awq_packed_sizes {
@@ -238,6 +239,128 @@ awq_status awq_dequant_fp8(const void* qweight, const void* scales, const void* 
 awq_status awq_w4a8_gemm(const void* x8, const void* sx, const void* qweight, const void* scales, const void* zeros,
                          const void* row_exp, void* y, int64_t M, int64_t K, int64_t N, int group, void* workspace,
                          size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Between the linear layers: RMS norm and gated SiLU
+ * ---------------------------------------------------------------------------
+ * What a decoder layer runs before its qkv and gate_up layers and between
+ * gate_up and down, with the output either in fp16 (for awq_linear) or in the
+ * E4M3 form that awq_w4a8_gemm takes: sx[m] = max_k |y[m][k]| / 448 (fp32) and
+ * x8[m][k] = e4m3(y[m][k] / sx[m]) (0 when sx[m] == 0). Inputs are fp16, all
+ * arithmetic is fp32 and y is rounded once, to fp16 or to E4M3 (so the E4M3
+ * form is not awq_fp8_quantize_x of the fp16 form, which rounds twice).
+ * Shapes: M >= 0 (0 is a no-op), K and F multiples of 8 (else AWQ_ERR_SHAPE),
+ * K, F <= 2^22, M <= 2^24, M * F <= 2^40 (else AWQ_ERR_UNSUPPORTED). Every
+ * pointer is 16-byte aligned. Outputs may not overlap inputs or one another
+ * (AWQ_ERR_INVALID_ARG), but for h below. A row that holds an infinity or a
+ * NaN gives a y, or an sx, that is not finite. */
+
+/* y = h * rsqrt(mean_k h^2 + eps) * weight, y fp16 [M][K], weight fp16 [K].
+ * With residual fp16 [M][K], h = x + residual, and h rounded to fp16 is
+ * written to h fp16 [M][K] (the next residual; y is made from the sum before
+ * that rounding). h may be the same buffer as x or residual. Without a
+ * residual (NULL), h = x and the argument h must be NULL too. eps >= 0.
+ * Source: none on the pages (the norm ahead of the linear layers). */
+awq_status awq_rmsnorm(const void* x, const void* residual, const void* weight, float eps, void* h, void* y,
+                       int64_t M, int64_t K, void* stream);
+
+/* awq_rmsnorm with y as E4M3 codes x8 uint8 [M][K] and scales sx fp32 [M].
+ * Source: TensorRT-LLM news item on INT4 AWQ on one H200 (FP8 compute). */
+awq_status awq_rmsnorm_fp8(const void* x, const void* residual, const void* weight, float eps, void* h, void* x8,
+                           void* sx, int64_t M, int64_t K, void* stream);
+
+/* y[m][f] = g / (1 + exp(-g)) * u with g = gate_up[m][f] and u =
+ * gate_up[m][F + f]: gate_up fp16 [M][2F], the output of one layer whose
+ * first F channels are the gate and whose last F the values; y fp16 [M][F].
+ * Source: none on the pages (the activation between gate_up and down). */
+awq_status awq_silu_mul(const void* gate_up, void* y, int64_t M, int64_t F, void* stream);
+
+/* awq_silu_mul with y as E4M3 codes x8 uint8 [M][F] and scales sx fp32 [M]. A
+ * row whose largest |y| is below 2^-100 counts as zero.
+ * Source: TensorRT-LLM news item on INT4 AWQ on one H200 (FP8 compute). */
+awq_status awq_silu_mul_fp8(const void* gate_up, void* x8, void* sx, int64_t M, int64_t F, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Between qkv and o_proj: an 8-bit key/value cache and its attention
+ * ---------------------------------------------------------------------------
+ * The cache is paged: `blocks` blocks of block_tokens tokens (16, 32, 64 or
+ * 128), each with every kv head (head_dim 64 or 128):
+ *   k, v          uint8 [blocks][heads][block_tokens][head_dim], E4M3 codes
+ *   k_exp, v_exp  int8  [blocks][heads]
+ *   value = code * 2^exp, one exponent per block and head
+ * A batch is `seqs` sequences. Sequence b owns rows starts[b] .. starts[b+1]-1
+ * of q, k, v and y (its new tokens; there may be none), has lens[b] tokens in
+ * all, the new ones being the last, and keeps token j in block
+ * table[b][j / block_tokens] at place j % block_tokens. So new row i of
+ * sequence b has position lens[b] - (starts[b+1] - starts[b]) + i; a row whose
+ * position is negative has no place in the cache and sees no key. Rows that
+ * belong to no sequence are neither read nor written.
+ * starts, lens and table are int32 in device memory, read when the kernels
+ * run, so a captured graph may be replayed with new contents. They need no
+ * alignment beyond their type's.
+ * Both calls check these contents as they run: starts outside 0 .. rows or
+ * decreasing, a length outside 0 .. table_width * block_tokens, or a block
+ * number in use outside 0 .. blocks-1 records AWQ_ERR_BOUNDS in the workspace
+ * status word. Bounds are clamped then, and tokens in such a block are not
+ * written and read as zeros; nothing outside the buffers is touched.
+ * Limits (AWQ_ERR_UNSUPPORTED): rows <= 2^24, seqs <= 2^20, seqs * heads <=
+ * 2^24, q_heads <= 4096, rows * q_heads < 2^31, blocks < 2^31, table_width *
+ * block_tokens <= 2^28. rows = 0 or seqs = 0 is a no-op.
+ * q, k and v may be column ranges of one matrix: row r starts at element r *
+ * stride, where the stride is a multiple of 8 and at least the row's width;
+ * the heads of a row are contiguous. */
+typedef struct awq_kv8_cache {
+  void *k, *v;          /* 16-byte aligned */
+  void *k_exp, *v_exp;
+  int64_t blocks;
+  int32_t heads, block_tokens, head_dim;
+} awq_kv8_cache;
+
+typedef struct awq_kv8_batch {
+  const void *starts;   /* int32 [seqs + 1] */
+  const void *lens;     /* int32 [seqs] */
+  const void *table;    /* int32 [seqs][table_width] */
+  int64_t rows, seqs, table_width;
+} awq_kv8_batch;
+
+/* Workspace bytes of awq_kv8_append and awq_kv8_attention for a batch of
+ * these sizes on the current device: the status word and the attention's fp32
+ * parts of rows that several CTAs work on. Set up and used like the workspace
+ * of the linear layers (awq_workspace_init once, one call at a time). Host
+ * only. 0 for invalid sizes.
+ * Source: none on the pages (the kernels' scratch memory, owned by the caller). */
+size_t awq_kv8_workspace_bytes(int64_t rows, int64_t seqs, int q_heads, int heads, int head_dim);
+
+/* Write the new tokens' k and v, fp16 [rows][heads][head_dim], into the cache.
+ * For each block and head that gets new tokens, exp becomes the smallest
+ * integer with |value| <= 448 * 2^exp for all new finite values (-32 if they
+ * are zero), but not less than it was if the block held tokens of the
+ * sequence already; then their codes are rewritten under the new exponent
+ * (rounded once more only where a code becomes an E4M3 subnormal). New codes
+ * are e4m3(value / 2^exp), round to nearest even; an infinity or a NaN becomes
+ * the NaN code. Places behind a sequence's end keep their contents. A block
+ * that gets new tokens must belong to one sequence only (full blocks may be
+ * shared). Calling it again with the same arguments leaves the cache as it is.
+ * Source: TinyChat README (pre-allocated KV cache); the 8-bit form is ours. */
+awq_status awq_kv8_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const awq_kv8_cache* cache, const awq_kv8_batch* batch, void* workspace, size_t ws_bytes,
+                          void* stream);
+
+/* Causal attention of the new rows over the cache (call it after
+ * awq_kv8_append): q fp16 [rows][q_heads][head_dim], y fp16
+ * [rows][q_heads * head_dim]; query head i reads kv head i / (q_heads /
+ * heads). The row at position p gives
+ *   y = sum_{j <= p} softmax_j(scale * q . k_j) v_j,
+ * and zeros when it sees no key. Made for the generation stage: one or a few
+ * new tokens per sequence. More are right too, but every 16 rows of a kv head
+ * read the sequence's keys anew. fp32 sums, the softmax weights rounded to
+ * fp16 for their product with v. Work is split along the keys as well; parts
+ * are added in a fixed order, so results are deterministic for a given device
+ * and batch. A NaN code gives NaN in the rows that see it.
+ * Source: TinyChat README (attention over the KV cache in the generation
+ * stage); the 8-bit form is ours. */
+awq_status awq_kv8_attention(const void* q, int64_t q_stride, int q_heads, float scale, const awq_kv8_cache* cache,
+                             const awq_kv8_batch* batch, void* y, void* workspace, size_t ws_bytes, void* stream);
 
 /* The M at and below which awq_linear always takes the GEMV path (above it,
  * up to AWQ_GEMV_MAX_M, only for layers with fewer 128-channel tiles than SMs).

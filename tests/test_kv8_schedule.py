@@ -1,0 +1,82 @@
+"""Host model of the cache attention's work split (csrc/kv8.cu): units of
+64 keys (128 for 64-wide heads) of one (sequence, kv head, row tile), equal
+contiguous ranges of them per CTA, and the hand-over of groups that several
+CTAs work on to the fixup kernel. Checked on random ragged batches: every unit
+is computed once, a group's rows are written once, by the CTA that computes
+all of it or by the fixup, and the fixup reads exactly the slots that the
+group's contributors wrote."""
+import random
+
+import pytest
+
+
+def plan(seqs, group, heads, rows_per_tile, keys_per_unit):
+    """(row_tiles, key_tiles) of every sequence (new tokens, length)."""
+    return [(-(-t * group // rows_per_tile), max(-(-n // keys_per_unit), 1)) for t, n in seqs]
+
+
+def simulate(seqs, group, heads, rows_per_tile, keys_per_unit, grid):
+    tiles = plan(seqs, group, heads, rows_per_tile, keys_per_unit)
+    total = sum(r * k * heads for r, k in tiles)
+    ctas = min(total, grid)
+    owner = {}      # unit -> CTA
+    direct = set()  # groups written by the attention kernel
+    slots = {}      # (cta, slot) -> group
+    fix = {}        # cta -> (group, last cta)
+    for c in range(ctas):
+        u = total // ctas * c + total % ctas * c // ctas
+        u1 = total // ctas * (c + 1) + total % ctas * (c + 1) // ctas
+        b, base = 0, 0
+        while u < u1:
+            while u >= base + tiles[b][0] * tiles[b][1] * heads:
+                base += tiles[b][0] * tiles[b][1] * heads
+                b += 1
+            rt, kt = tiles[b]
+            g, tile0 = divmod(u - base, kt)
+            h, row_tile = divmod(g, rt)
+            n = min(u1 - u, kt - tile0)
+            for i in range(n):
+                assert u + i not in owner
+                owner[u + i] = c
+            who = (b, h, row_tile)
+            assert 0 <= h < heads and 0 <= row_tile < rt
+            if tile0 == 0 and n == kt:
+                assert who not in direct
+                direct.add(who)
+            else:
+                key = (c, 1 if tile0 == 0 else 0)
+                assert key not in slots
+                slots[key] = who
+                if tile0 == 0:
+                    end = u + kt
+                    assert c not in fix
+                    fix[c] = (who, (end * ctas + total - 1) // total - 1)
+            u += n
+    assert sorted(owner) == list(range(total))
+    fixed = set()
+    for c, (who, last) in fix.items():
+        assert last > c
+        for i in range(c, last + 1):
+            assert slots.pop((i, 1 if i == c else 0)) == who
+        assert who not in fixed and who not in direct
+        fixed.add(who)
+    assert not slots
+    groups = {(b, h, r) for b, (rt, _) in enumerate(tiles) for h in range(heads) for r in range(rt)}
+    assert direct | fixed == groups
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_every_unit_once_and_every_group_written_once(seed):
+    rng = random.Random(seed)
+    for _ in range(25):
+        B = rng.randint(1, 20)
+        seqs = [(rng.choice([0, 1, 1, 1, rng.randint(2, 40)]), rng.choice([0, 1, rng.randint(1, 300), rng.randint(1, 9000)]))
+                for _ in range(B)]
+        simulate(seqs, rng.choice([1, 4, 8, 29]), rng.choice([1, 2, 8]), rng.choice([8, 16]), rng.choice([64, 128]),
+                 rng.choice([1, 3, 148, 444, 592]))
+
+
+def test_long_and_empty_batches():
+    simulate([(1, 131072)], 4, 8, 8, 64, 592)
+    simulate([(0, 0), (0, 50), (1, 0)], 4, 8, 8, 64, 592)
+    simulate([(0, 0)], 4, 8, 8, 64, 592)

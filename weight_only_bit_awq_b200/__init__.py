@@ -13,12 +13,15 @@ Functions (same names as the C entry points):
   awq_get_status, awq_status_string, awq_w4a16_gemv_no_alloc,
   awq_get_status_no_alloc, and the W4A8-FP8
   variant awq_fp8_row_exponents, awq_fp8_quantize_x, awq_dequant_fp8,
-  awq_w4a8_gemm.
+  awq_w4a8_gemm. Between the linear layers: awq_rmsnorm, awq_rmsnorm_fp8,
+  awq_silu_mul, awq_silu_mul_fp8, and the 8-bit key/value cache
+  awq_kv8_workspace_bytes, awq_kv8_append, awq_kv8_attention.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -43,7 +46,9 @@ EXPORTS = ("awq_packed_size", "awq_workspace_bytes", "awq_workspace_init", "awq_
            "awq_status_string", "awq_w4a16_gemv_no_alloc", "awq_get_status_no_alloc", "awq_linear_launches",
            "awq_linear_path",
            "awq_check_bounded_wait",
-           "awq_fp8_row_exponents", "awq_fp8_quantize_x", "awq_dequant_fp8", "awq_w4a8_gemm")
+           "awq_fp8_row_exponents", "awq_fp8_quantize_x", "awq_dequant_fp8", "awq_w4a8_gemm",
+           "awq_rmsnorm", "awq_rmsnorm_fp8", "awq_silu_mul", "awq_silu_mul_fp8",
+           "awq_kv8_workspace_bytes", "awq_kv8_append", "awq_kv8_attention")
 
 
 class AwqError(RuntimeError):
@@ -55,6 +60,17 @@ class AwqError(RuntimeError):
 class _PackedSizes(ctypes.Structure):
     _fields_ = [("qweight_bytes", ctypes.c_size_t), ("scales_bytes", ctypes.c_size_t),
                 ("zeros_bytes", ctypes.c_size_t)]
+
+
+class _Kv8Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("blocks", ctypes.c_int64), ("heads", ctypes.c_int32), ("block_tokens", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class _Kv8Batch(ctypes.Structure):
+    _fields_ = [("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("seqs", ctypes.c_int64), ("table_width", ctypes.c_int64)]
 
 
 def _build_module():
@@ -91,10 +107,20 @@ def _load() -> ctypes.CDLL:
     lib.awq_fp8_quantize_x.argtypes = [vp, i64, i64, vp, vp, vp]
     lib.awq_dequant_fp8.argtypes = [vp, vp, vp, vp, i64, i64, ci, vp, vp]
     lib.awq_w4a8_gemm.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, vp, sz, vp]
+    cf = ctypes.c_float
+    lib.awq_rmsnorm.argtypes = [vp, vp, vp, cf, vp, vp, i64, i64, vp]
+    lib.awq_rmsnorm_fp8.argtypes = [vp, vp, vp, cf, vp, vp, vp, i64, i64, vp]
+    lib.awq_silu_mul.argtypes = [vp, vp, i64, i64, vp]
+    lib.awq_silu_mul_fp8.argtypes = [vp, vp, vp, i64, i64, vp]
+    pc, pb = ctypes.POINTER(_Kv8Cache), ctypes.POINTER(_Kv8Batch)
+    lib.awq_kv8_workspace_bytes.argtypes = [i64, i64, ci, ci, ci]
+    lib.awq_kv8_workspace_bytes.restype = sz
+    lib.awq_kv8_append.argtypes = [vp, i64, vp, i64, pc, pb, vp, sz, vp]
+    lib.awq_kv8_attention.argtypes = [vp, i64, ci, cf, pc, pb, vp, vp, sz, vp]
     lib.awq_status_string.argtypes = [ci]
     lib.awq_status_string.restype = ctypes.c_char_p
     for f in EXPORTS:
-        if f not in ("awq_workspace_bytes", "awq_status_string"):
+        if f not in ("awq_workspace_bytes", "awq_kv8_workspace_bytes", "awq_status_string"):
             getattr(lib, f).restype = ci
     return lib
 
@@ -262,6 +288,185 @@ def awq_w4a8_gemm(x8, sx, qweight, scales, zeros, row_exp, N, workspace, group: 
                              _dev(zeros, torch.uint8, "zeros"), _dev(row_exp, torch.int8, "row_exp"),
                              _dev(y, torch.float16, "y"), M, K, N, group, _dev(workspace, torch.uint8, "workspace"),
                              workspace.numel(), _stream(x8)), "awq_w4a8_gemm")
+    return y
+
+
+def _call(fn, name: str, tensors, *args):
+    """fn(*args, stream) on the device of the tensors (which must share one),
+    on that device's current stream."""
+    device = tensors[0].device
+    for t in tensors:
+        if t.device != device:
+            raise ValueError(f"{name}: tensors on {device} and {t.device}")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), name)
+
+
+def _out(t, shape, dtype, name: str, device) -> torch.Tensor:
+    """The output `t`, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    _dev(t, dtype, name)
+    return t
+
+
+def _norm_inputs(x, weight, residual, h):
+    M, K = x.shape
+    tensors = [x, weight]
+    px, pw = _dev(x, torch.float16, "x"), _dev(weight, torch.float16, "weight")
+    if weight.shape != (K,):
+        raise ValueError(f"weight must be [{K}]")
+    if residual is None:
+        if h is not None:
+            raise ValueError("h needs a residual")
+        return M, K, tensors, px, None, pw, None
+    pr = _dev(residual, torch.float16, "residual")
+    if residual.shape != (M, K):
+        raise ValueError(f"residual must be [{M}, {K}]")
+    h = _out(h, (M, K), torch.float16, "h", x.device)
+    return M, K, tensors + [residual, h], px, pr, pw, h
+
+
+def awq_rmsnorm(x, weight, eps: float, residual=None, h=None, y=None):
+    """y fp16 [M][K] = n * rsqrt(mean(n^2) + eps) * weight with n = x, or with a
+    residual n = x + residual; then (y, h) is returned, h = n rounded to fp16
+    (h may be x or residual itself: updated in place)."""
+    M, K, tensors, px, pr, pw, h = _norm_inputs(x, weight, residual, h)
+    y = _out(y, (M, K), torch.float16, "y", x.device)
+    _call(lib.awq_rmsnorm, "awq_rmsnorm", tensors + [y], px, pr, pw, eps, None if h is None else h.data_ptr(),
+          y.data_ptr(), M, K)
+    return y if h is None else (y, h)
+
+
+def awq_rmsnorm_fp8(x, weight, eps: float, residual=None, h=None, x8=None, sx=None):
+    """awq_rmsnorm with y as (x8 uint8 E4M3 codes [M][K], sx float32 [M]), the
+    inputs of awq_w4a8_gemm; (x8, sx, h) with a residual."""
+    M, K, tensors, px, pr, pw, h = _norm_inputs(x, weight, residual, h)
+    x8 = _out(x8, (M, K), torch.uint8, "x8", x.device)
+    sx = _out(sx, (M,), torch.float32, "sx", x.device)
+    _call(lib.awq_rmsnorm_fp8, "awq_rmsnorm_fp8", tensors + [x8, sx], px, pr, pw, eps,
+          None if h is None else h.data_ptr(), x8.data_ptr(), sx.data_ptr(), M, K)
+    return (x8, sx) if h is None else (x8, sx, h)
+
+
+def _gate_up(gate_up):
+    M, F2 = gate_up.shape
+    if F2 % 2:
+        raise ValueError("gate_up must be [M, 2F]")
+    return M, F2 // 2, _dev(gate_up, torch.float16, "gate_up")
+
+
+def awq_silu_mul(gate_up, y=None):
+    """gate_up fp16 [M][2F] -> y fp16 [M][F] = silu(gate_up[:, :F]) * gate_up[:, F:]."""
+    M, F, p = _gate_up(gate_up)
+    y = _out(y, (M, F), torch.float16, "y", gate_up.device)
+    _call(lib.awq_silu_mul, "awq_silu_mul", (gate_up, y), p, y.data_ptr(), M, F)
+    return y
+
+
+def awq_silu_mul_fp8(gate_up, x8=None, sx=None):
+    """awq_silu_mul with y as (x8 uint8 E4M3 codes [M][F], sx float32 [M]), the
+    inputs of awq_w4a8_gemm."""
+    M, F, p = _gate_up(gate_up)
+    x8 = _out(x8, (M, F), torch.uint8, "x8", gate_up.device)
+    sx = _out(sx, (M,), torch.float32, "sx", gate_up.device)
+    _call(lib.awq_silu_mul_fp8, "awq_silu_mul_fp8", (gate_up, x8, sx), p, x8.data_ptr(), sx.data_ptr(), M, F)
+    return x8, sx
+
+
+class Kv8Cache(NamedTuple):
+    """An 8-bit key/value cache: E4M3 codes uint8 [blocks][heads][block_tokens]
+    [head_dim] and their exponents int8 [blocks][heads]; value = code * 2^exp."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_exp: torch.Tensor
+    v_exp: torch.Tensor
+
+
+def new_kv8_cache(blocks: int, heads: int, block_tokens: int, head_dim: int, device) -> Kv8Cache:
+    """Allocate (with torch) an empty cache."""
+    codes = (blocks, heads, block_tokens, head_dim)
+    return Kv8Cache(torch.zeros(codes, dtype=torch.uint8, device=device),
+                    torch.zeros(codes, dtype=torch.uint8, device=device),
+                    torch.zeros(codes[:2], dtype=torch.int8, device=device),
+                    torch.zeros(codes[:2], dtype=torch.int8, device=device))
+
+
+def awq_kv8_workspace_bytes(rows: int, seqs: int, q_heads: int, heads: int, head_dim: int) -> int:
+    return int(lib.awq_kv8_workspace_bytes(rows, seqs, q_heads, heads, head_dim))
+
+
+def new_kv8_workspace(rows: int, seqs: int, q_heads: int, heads: int, head_dim: int, device) -> torch.Tensor:
+    """Allocate (with torch) and zero a workspace for awq_kv8_append and awq_kv8_attention."""
+    with torch.cuda.device(device):
+        nbytes = awq_kv8_workspace_bytes(rows, seqs, q_heads, heads, head_dim)
+        if nbytes == 0:
+            raise AwqError(AWQ_ERR_SHAPE, "awq_kv8_workspace_bytes")
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        awq_workspace_init(ws)
+    return ws
+
+
+def _kv8_rows(t, rows, heads, head_dim, name):
+    """Pointer and row stride of fp16 [rows][heads][head_dim] whose rows may lie
+    apart (a column range of a wider matrix)."""
+    if not t.is_cuda or t.dtype != torch.float16:
+        raise ValueError(f"{name} must be a CUDA tensor of torch.float16")
+    if tuple(t.shape) != (rows, heads, head_dim):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {head_dim}]")
+    stride = t.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (stride[0] if rows > 1 else heads * head_dim)
+
+
+def _kv8_call(fn, name, rows, cache, starts, lens, table, workspace, tensors, before, after):
+    k, v, k_exp, v_exp = cache
+    blocks, heads, block_tokens, head_dim = k.shape
+    if v.shape != k.shape or k_exp.shape != k.shape[:2] or v_exp.shape != k.shape[:2]:
+        raise ValueError("cache parts must be [blocks, heads, block_tokens, head_dim] and [blocks, heads]")
+    c = _Kv8Cache(_dev(k, torch.uint8, "cache.k"), _dev(v, torch.uint8, "cache.v"),
+                  _dev(k_exp, torch.int8, "cache.k_exp"), _dev(v_exp, torch.int8, "cache.v_exp"), blocks, heads,
+                  block_tokens, head_dim)
+    seqs, width = table.shape
+    if starts.shape != (seqs + 1,) or lens.shape != (seqs,):
+        raise ValueError(f"starts must be [{seqs + 1}] and lens [{seqs}]")
+    b = _Kv8Batch(_dev(starts, torch.int32, "starts"), _dev(lens, torch.int32, "lens"),
+                  _dev(table, torch.int32, "block_table"), rows, seqs, width)
+    _call(fn, name, (k, v, k_exp, v_exp, starts, lens, table, workspace, *tensors), *before, ctypes.byref(c),
+          ctypes.byref(b), *after, _dev(workspace, torch.uint8, "workspace"), workspace.numel())
+
+
+def awq_kv8_append(k, v, cache: Kv8Cache, starts, lens, block_table, workspace):
+    """Write the new tokens' k and v, fp16 [rows][heads][head_dim], into the
+    cache: sequence b owns rows starts[b] .. starts[b+1]-1, has lens[b] tokens
+    with them (the last ones), and its token j lies in block
+    block_table[b][j // block_tokens] (int32 tensors; see include/awq.h)."""
+    heads, head_dim = cache[0].shape[1], cache[0].shape[3]
+    rows = k.shape[0]
+    pk, sk = _kv8_rows(k, rows, heads, head_dim, "k")
+    pv, sv = _kv8_rows(v, rows, heads, head_dim, "v")
+    _kv8_call(lib.awq_kv8_append, "awq_kv8_append", rows, cache, starts, lens, block_table, workspace, (k, v),
+              (pk, sk, pv, sv), ())
+
+
+def awq_kv8_attention(q, cache: Kv8Cache, starts, lens, block_table, workspace, scale: float | None = None, y=None):
+    """Causal attention of the new rows q fp16 [rows][q_heads][head_dim] over the
+    cache (after awq_kv8_append, same starts, lens and block_table): y fp16
+    [rows][q_heads * head_dim]. scale: 1 / sqrt(head_dim) unless given. Rows
+    of y that belong to no sequence are not written."""
+    rows, q_heads, head_dim = q.shape
+    if head_dim != cache[0].shape[3]:
+        raise ValueError(f"q must be [rows, q_heads, {cache[0].shape[3]}]")
+    pq, sq = _kv8_rows(q, rows, q_heads, head_dim, "q")
+    y = _out(y, (rows, q_heads * head_dim), torch.float16, "y", q.device)
+    _kv8_call(lib.awq_kv8_attention, "awq_kv8_attention", rows, cache, starts, lens, block_table, workspace, (q, y),
+              (pq, sq, q_heads, head_dim ** -0.5 if scale is None else scale), (y.data_ptr(),))
     return y
 
 

@@ -1,5 +1,6 @@
 // C ABI entry points of libawq_b200.so (declared in include/awq.h): argument
 // checks, workspace layout, dispatch between the GEMV and GEMM paths.
+#include <cfloat>
 #include <mutex>
 
 #include "awq_internal.cuh"
@@ -162,6 +163,137 @@ constexpr int kGemvAlwaysM = 16;
 
 bool linear_uses_gemv(int64_t M, int64_t N, int sm_count) {
   return M <= kGemvAlwaysM || (M <= AWQ_GEMV_MAX_M && (N + 127) / 128 < sm_count);
+}
+
+// Shared checks of the norm and the SiLU: `in` inputs, `out` outputs.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+awq_status check_spans(const Span* in, int n_in, const Span* out, int n_out) {
+  for (int i = 0; i < n_in; ++i)
+    if (!in[i].p) return AWQ_ERR_INVALID_ARG;
+  for (int i = 0; i < n_out; ++i)
+    if (!out[i].p) return AWQ_ERR_INVALID_ARG;
+  for (int i = 0; i < n_in; ++i)
+    if (!aligned16(in[i].p)) return AWQ_ERR_ALIGNMENT;
+  for (int i = 0; i < n_out; ++i)
+    if (!aligned16(out[i].p)) return AWQ_ERR_ALIGNMENT;
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return AWQ_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return AWQ_ERR_INVALID_ARG;
+  }
+  return AWQ_OK;
+}
+
+awq_status rmsnorm_impl(const void* x, const void* residual, const void* weight, float eps, void* h, void* y, void* x8,
+                        void* sx, bool fp8, int64_t M, int64_t K, void* stream) {
+  if (M < 0 || K <= 0 || K % 8 != 0) return AWQ_ERR_SHAPE;
+  if (K > kMaxK || M > kMaxM) return AWQ_ERR_UNSUPPORTED;
+  if (!(eps >= 0.f && eps <= FLT_MAX) || (residual == nullptr) != (h == nullptr)) return AWQ_ERR_INVALID_ARG;
+  if (M == 0) return AWQ_OK;
+  const size_t n = (size_t)M * K;
+  const Span in[3] = {{x, 2 * n}, {weight, (size_t)K * 2}, {residual, 2 * n}};
+  const Span out[2] = {{fp8 ? x8 : y, fp8 ? n : 2 * n}, {sx, (size_t)M * 4}};
+  awq_status st = check_spans(in, residual ? 3 : 2, out, fp8 ? 2 : 1);
+  if (st != AWQ_OK) return st;
+  if (h) {
+    if (!aligned16(h)) return AWQ_ERR_ALIGNMENT;
+    // every thread reads its elements of x and residual before it writes the same ones of h
+    if ((h != x && overlap(h, 2 * n, x, 2 * n)) || (h != residual && overlap(h, 2 * n, residual, 2 * n)) ||
+        overlap(h, 2 * n, weight, (size_t)K * 2) || overlap(h, 2 * n, out[0].p, out[0].bytes) ||
+        (fp8 && overlap(h, 2 * n, sx, (size_t)M * 4)))
+      return AWQ_ERR_INVALID_ARG;
+  }
+  if ((st = check_device()) != AWQ_OK) return st;
+  cudaError_t e = launch_rmsnorm(static_cast<const __half*>(x), static_cast<const __half*>(residual),
+                                 static_cast<const __half*>(weight), eps, static_cast<__half*>(h),
+                                 static_cast<__half*>(y), static_cast<uint8_t*>(x8), static_cast<float*>(sx), M, K,
+                                 static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
+awq_status silu_impl(const void* gate_up, void* y, void* x8, void* sx, bool fp8, int64_t M, int64_t F, void* stream) {
+  if (M < 0 || F <= 0 || F % 8 != 0) return AWQ_ERR_SHAPE;
+  if (F > kMaxK || M > kMaxM || M * F > int64_t(1) << 40) return AWQ_ERR_UNSUPPORTED;
+  if (M == 0) return AWQ_OK;
+  const size_t n = (size_t)M * F;
+  const Span in[1] = {{gate_up, 4 * n}};
+  const Span out[2] = {{fp8 ? x8 : y, fp8 ? n : 2 * n}, {sx, (size_t)M * 4}};
+  awq_status st = check_spans(in, 1, out, fp8 ? 2 : 1);
+  if (st != AWQ_OK) return st;
+  if ((st = check_device()) != AWQ_OK) return st;
+  cudaError_t e = launch_silu_mul(static_cast<const __half*>(gate_up), static_cast<__half*>(y),
+                                  static_cast<uint8_t*>(x8), static_cast<float*>(sx), M, F,
+                                  static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
+constexpr int kMaxHeads = 4096;
+
+awq_status check_kv8_sizes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t head_dim) {
+  if (rows < 0 || seqs < 0 || q_heads <= 0 || heads <= 0 || q_heads % heads != 0) return AWQ_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return AWQ_ERR_UNSUPPORTED;
+  if (rows > kMaxM || seqs > int64_t(1) << 20 || q_heads > kMaxHeads || seqs * heads > int64_t(1) << 24 ||
+      rows * q_heads > 0x7FFFFFFF)
+    return AWQ_ERR_UNSUPPORTED;
+  return AWQ_OK;
+}
+
+// The cache and batch of a call, checked, as the kernels take them.
+awq_status check_kv8(const awq_kv8_cache* cache, const awq_kv8_batch* batch, int64_t q_heads, const void* workspace,
+                     size_t ws_bytes, Kv8Cache* c, Kv8Batch* b) {
+  if (!cache || !batch) return AWQ_ERR_INVALID_ARG;
+  awq_status st = check_kv8_sizes(batch->rows, batch->seqs, q_heads, cache->heads, cache->head_dim);
+  if (st != AWQ_OK) return st;
+  if (cache->blocks < 0 || batch->table_width < 0) return AWQ_ERR_SHAPE;
+  const int bs = cache->block_tokens;
+  if (bs != 16 && bs != 32 && bs != 64 && bs != 128) return AWQ_ERR_UNSUPPORTED;
+  if (cache->blocks > 0x7FFFFFFF || batch->table_width > (int64_t(1) << 28) / bs) return AWQ_ERR_UNSUPPORTED;
+  *b = Kv8Batch{};
+  if (batch->rows == 0 || batch->seqs == 0) return AWQ_OK;  // nothing is read or written: pointers may be null
+  if (!cache->k || !cache->v || !cache->k_exp || !cache->v_exp || !batch->starts || !batch->lens || !batch->table || !workspace)
+    return AWQ_ERR_INVALID_ARG;
+  if (cache->blocks == 0 || batch->table_width == 0) return AWQ_ERR_SHAPE;
+  if (!aligned16(cache->k) || !aligned16(cache->v) || !aligned16(workspace) ||
+      ((reinterpret_cast<uintptr_t>(batch->starts) | reinterpret_cast<uintptr_t>(batch->lens) |
+        reinterpret_cast<uintptr_t>(batch->table)) & 3u) != 0)
+    return AWQ_ERR_ALIGNMENT;
+  if (ws_bytes < awq_kv8_workspace_bytes(batch->rows, batch->seqs, (int)q_heads, cache->heads, cache->head_dim))
+    return AWQ_ERR_WORKSPACE;
+  *c = Kv8Cache{static_cast<uint8_t*>(cache->k), static_cast<uint8_t*>(cache->v), static_cast<int8_t*>(cache->k_exp),
+                static_cast<int8_t*>(cache->v_exp), cache->blocks, cache->heads, cache->head_dim};
+  *b = Kv8Batch{static_cast<const int*>(batch->starts), static_cast<const int*>(batch->lens),
+                static_cast<const int*>(batch->table), (int)batch->seqs, (int)batch->rows, (int)batch->table_width, bs};
+  const Span parts[5] = {{c->k, (size_t)c->blocks * c->heads * bs * c->head_dim},
+                         {c->v, (size_t)c->blocks * c->heads * bs * c->head_dim},
+                         {c->k_exp, (size_t)c->blocks * c->heads},
+                         {c->v_exp, (size_t)c->blocks * c->heads},
+                         {workspace, ws_bytes}};
+  const Span lists[3] = {{b->starts, (size_t)(b->seqs + 1) * 4},
+                         {b->lens, (size_t)b->seqs * 4},
+                         {b->table, (size_t)b->seqs * b->table_width * 4}};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(parts[i].p, parts[i].bytes, parts[j].p, parts[j].bytes)) return AWQ_ERR_INVALID_ARG;
+    for (int j = 0; j < 3; ++j)
+      if (overlap(parts[i].p, parts[i].bytes, lists[j].p, lists[j].bytes)) return AWQ_ERR_INVALID_ARG;
+  }
+  return AWQ_OK;
+}
+
+// Bytes from the first element of a strided matrix to its last.
+size_t row_bytes(int64_t rows, int64_t stride, int64_t width) { return (size_t)((rows - 1) * stride + width) * 2; }
+
+// Whether [p, p + bytes) touches the cache or the batch's lists.
+bool kv8_overlap(const Kv8Cache& c, const Kv8Batch& b, const void* p, size_t bytes) {
+  const size_t codes = (size_t)c.blocks * c.heads * b.block_tokens * c.head_dim, exps = (size_t)c.blocks * c.heads;
+  return overlap(p, bytes, c.k, codes) || overlap(p, bytes, c.v, codes) || overlap(p, bytes, c.k_exp, exps) ||
+         overlap(p, bytes, c.v_exp, exps) || overlap(p, bytes, b.starts, (size_t)(b.seqs + 1) * 4) ||
+         overlap(p, bytes, b.lens, (size_t)b.seqs * 4) || overlap(p, bytes, b.table, (size_t)b.seqs * b.table_width * 4);
 }
 
 }  // namespace
@@ -345,6 +477,73 @@ awq_status awq_w4a8_gemm(const void* x8, const void* sx, const void* qweight, co
   return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
 }
 
+awq_status awq_rmsnorm(const void* x, const void* residual, const void* weight, float eps, void* h, void* y, int64_t M,
+                       int64_t K, void* stream) {
+  return rmsnorm_impl(x, residual, weight, eps, h, y, nullptr, nullptr, false, M, K, stream);
+}
+
+awq_status awq_rmsnorm_fp8(const void* x, const void* residual, const void* weight, float eps, void* h, void* x8,
+                           void* sx, int64_t M, int64_t K, void* stream) {
+  return rmsnorm_impl(x, residual, weight, eps, h, nullptr, x8, sx, true, M, K, stream);
+}
+
+awq_status awq_silu_mul(const void* gate_up, void* y, int64_t M, int64_t F, void* stream) {
+  return silu_impl(gate_up, y, nullptr, nullptr, false, M, F, stream);
+}
+
+awq_status awq_silu_mul_fp8(const void* gate_up, void* x8, void* sx, int64_t M, int64_t F, void* stream) {
+  return silu_impl(gate_up, nullptr, x8, sx, true, M, F, stream);
+}
+
+size_t awq_kv8_workspace_bytes(int64_t rows, int64_t seqs, int q_heads, int heads, int head_dim) {
+  if (check_kv8_sizes(rows, seqs, q_heads, heads, head_dim) != AWQ_OK) return 0;
+  return kv8_workspace_bytes(head_dim, sm_count_or_default());
+}
+
+awq_status awq_kv8_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const awq_kv8_cache* cache, const awq_kv8_batch* batch, void* workspace, size_t ws_bytes,
+                          void* stream) {
+  Kv8Cache c;
+  Kv8Batch b;
+  awq_status st = check_kv8(cache, batch, cache ? cache->heads : 0, workspace, ws_bytes, &c, &b);
+  if (st != AWQ_OK) return st;
+  if (b.rows == 0) return AWQ_OK;
+  const int64_t width = (int64_t)c.heads * c.head_dim;
+  if (k_stride < width || v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0) return AWQ_ERR_SHAPE;
+  if (!k || !v) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return AWQ_ERR_ALIGNMENT;
+  const size_t kbytes = row_bytes(b.rows, k_stride, width), vbytes = row_bytes(b.rows, v_stride, width);
+  if (kv8_overlap(c, b, k, kbytes) || kv8_overlap(c, b, v, vbytes) || overlap(k, kbytes, workspace, ws_bytes) ||
+      overlap(v, vbytes, workspace, ws_bytes))
+    return AWQ_ERR_INVALID_ARG;
+  if ((st = check_device()) != AWQ_OK) return st;
+  cudaError_t e = launch_kv8_append(static_cast<const __half*>(k), static_cast<const __half*>(v), k_stride, v_stride, c, b,
+                                    status_word(workspace), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
+awq_status awq_kv8_attention(const void* q, int64_t q_stride, int q_heads, float scale, const awq_kv8_cache* cache,
+                             const awq_kv8_batch* batch, void* y, void* workspace, size_t ws_bytes, void* stream) {
+  Kv8Cache c;
+  Kv8Batch b;
+  awq_status st = check_kv8(cache, batch, q_heads, workspace, ws_bytes, &c, &b);
+  if (st != AWQ_OK) return st;
+  if (b.rows == 0) return AWQ_OK;
+  const int64_t width = (int64_t)q_heads * c.head_dim;
+  if (q_stride < width || q_stride % 8 != 0) return AWQ_ERR_SHAPE;
+  if (!(scale >= -FLT_MAX && scale <= FLT_MAX)) return AWQ_ERR_INVALID_ARG;
+  if (!q || !y) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(y)) return AWQ_ERR_ALIGNMENT;
+  const size_t ybytes = (size_t)b.rows * width * 2, qbytes = row_bytes(b.rows, q_stride, width);
+  if (kv8_overlap(c, b, y, ybytes) || overlap(y, ybytes, q, qbytes) || overlap(y, ybytes, workspace, ws_bytes) ||
+      overlap(q, qbytes, workspace, ws_bytes))
+    return AWQ_ERR_INVALID_ARG;
+  if ((st = check_device()) != AWQ_OK) return st;
+  cudaError_t e = launch_kv8_attention(static_cast<const __half*>(q), q_stride, q_heads, scale, c, b,
+                                       static_cast<__half*>(y), workspace, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
 int awq_linear_path(int64_t M, int64_t K, int64_t N, int group) {
   if (M <= 0 || M > kMaxM || check_kn(K, N, group) != AWQ_OK) return 0;
   const int sms = sm_count_or_default();
@@ -391,7 +590,7 @@ const char* awq_status_string(awq_status status) {
     case AWQ_ERR_CUDA: return "AWQ_ERR_CUDA: a CUDA call or kernel launch failed";
     case AWQ_ERR_TIMEOUT: return "AWQ_ERR_TIMEOUT: a bounded wait on the device expired";
     case AWQ_ERR_NONFINITE: return "AWQ_ERR_NONFINITE: awq_pack met an inf or NaN weight";
-    case AWQ_ERR_BOUNDS: return "AWQ_ERR_BOUNDS: a device-side index check of the debug build failed";
+    case AWQ_ERR_BOUNDS: return "AWQ_ERR_BOUNDS: a bad block number, row start or length of a cache batch, or a failed index check of the debug build";
   }
   return "unknown awq_status";
 }

@@ -142,6 +142,30 @@ cudaError_t launch_gemm_fp8(const uint8_t* x8, const float* sx, const uint32_t* 
                             const uint8_t* zeros, const int8_t* row_exp, __half* y, int64_t M, int64_t K, int64_t N,
                             int group, uint32_t* status, cudaStream_t stream);
 
+// The steps around the linear layers (norm_act.cu). Exactly one of y and x8
+// (with sx) is given; h is given with the residual.
+cudaError_t launch_rmsnorm(const __half* x, const __half* residual, const __half* w, float eps, __half* h, __half* y,
+                           uint8_t* x8, float* sx, int64_t M, int64_t K, cudaStream_t stream);
+cudaError_t launch_silu_mul(const __half* gate_up, __half* y, uint8_t* x8, float* sx, int64_t M, int64_t F,
+                            cudaStream_t stream);
+
+// The 8-bit key/value cache and its attention (kv8.cu).
+struct Kv8Cache {
+  uint8_t *k, *v;          // E4M3 codes [blocks][heads][block_tokens][head_dim]
+  int8_t *k_exp, *v_exp;   // [blocks][heads]
+  int64_t blocks;
+  int heads, head_dim;
+};
+struct Kv8Batch {
+  const int *starts, *lens, *table;  // [seqs + 1], [seqs], [seqs][table_width]
+  int seqs, rows, table_width, block_tokens;
+};
+size_t kv8_workspace_bytes(int head_dim, int sm_count);
+cudaError_t launch_kv8_append(const __half* k, const __half* v, int64_t k_stride, int64_t v_stride,
+                              const Kv8Cache& cache, const Kv8Batch& batch, uint32_t* status, cudaStream_t stream);
+cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads, float scale, const Kv8Cache& cache,
+                                 const Kv8Batch& batch, __half* out, void* workspace, cudaStream_t stream);
+
 // Packed word order inside a row's 128-input block, for group size G (128, 64
 // or 32): word w = 4t + j holds the eight inputs from k0(w) = G (j / J) +
 // 8 (t J + j % J), J = G / 32 (for G = 128 simply 8w). The four words with the

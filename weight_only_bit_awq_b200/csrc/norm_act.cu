@@ -1,0 +1,383 @@
+// The elementwise steps around a decoder layer's 4-bit linear layers:
+// awq_rmsnorm(_fp8) and awq_silu_mul(_fp8).
+//
+//   h = x + residual,  y = h * rsqrt(sum_k h^2 / K + eps) * w       (rmsnorm)
+//   y = g / (1 + 2^(-g log2 e)) * u,  gate_up row = [g | u]         (silu_mul)
+//   fp16:  y rounded once;   fp8:  sx = max_k|y| / 448, x8 = e4m3(y / sx)
+//
+// All sums and products are fp32; y is rounded once, to the output's type.
+// Both are bound by HBM (8 or 7 bytes an element for the norm with a
+// residual, 6 or 5 for the SiLU) and, at a few rows, by the launch.
+//
+// A row that needs a sum or a maximum is held in registers by one CTA: every
+// element is read once, between the load and the store there is one block
+// reduction. The norm's E4M3 form needs no second one: with m = max_k|h w|,
+// y / sx = h w 448 / m whatever the root mean square is.
+#include <cuda_fp8.h>
+
+#include "awq_internal.cuh"
+#include "sm100_ptx.cuh"
+
+namespace awq {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+// The codes of v * f; all zero (not minus zero) for f = 0, the factor of a row of zeros.
+__device__ __forceinline__ uint2 codes8(float (&v)[8], float f) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= f;
+  return f == 0.f ? make_uint2(0, 0) : make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ float2 h2f(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ uint32_t f2h(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const float2 a = h2f(v.x), b = h2f(v.y), c = h2f(v.z), d = h2f(v.w);
+  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y, f[4] = c.x, f[5] = c.y, f[6] = d.x, f[7] = d.y;
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(f2h(f[0], f[1]), f2h(f[2], f[3]), f2h(f[4], f[5]), f2h(f[6], f[7]));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Sum of `s` and maximum of `m` over the CTA; `red` holds two buffers that
+// alternate from row to row, so one barrier a row is enough.
+__device__ __forceinline__ void block_sum_max(float& s, float& m, float2* red, int parity) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  red += 32 * parity;
+  if (lane == 0) red[threadIdx.x >> 5] = make_float2(s, m);
+  __syncthreads();
+  const float2 v = lane < warps ? red[lane] : make_float2(0.f, 0.f);
+  s = v.x;
+  m = v.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+}
+
+struct NormArgs {
+  const __half *x, *residual, *w;
+  __half *h, *y;
+  uint8_t* x8;
+  float* sx;
+  float eps;
+  int64_t M;
+  int K8;  // 8-element vectors of a row
+};
+
+// The row factor of y (fp16 output) or of the codes (E4M3 output, where the
+// row's scale is stored too). A row with an infinity or a NaN has a sum that
+// is not finite: its y, or its sx, is not finite either.
+template <bool kFp8>
+__device__ __forceinline__ float norm_factor(const NormArgs& a, int64_t row, float sum, float mx) {
+  const float rs = rsqrtf(sum / (float)((int64_t)a.K8 * 8) + a.eps);
+  if (!kFp8) return rs;
+  if (threadIdx.x == 0) a.sx[row] = sum - sum == 0.f ? mx * rs * (1.f / kE4m3Max) : sum - sum;
+  return mx > 0.f ? kE4m3Max / mx : 0.f;
+}
+
+// One CTA a row at a time, the row in V vectors of 8 per thread.
+template <int V, bool kRes, bool kFp8>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
+  __shared__ float2 red[64];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int NT = blockDim.x, tid = threadIdx.x;
+  uint4 w[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = i * NT + tid;
+    w[i] = c < a.K8 ? reinterpret_cast<const uint4*>(a.w)[c] : make_uint4(0, 0, 0, 0);
+  }
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
+    const int64_t base = row * a.K8;
+    uint4 vx[V], vr[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = i * NT + tid;
+      vx[i] = c < a.K8 ? reinterpret_cast<const uint4*>(a.x)[base + c] : make_uint4(0, 0, 0, 0);
+      if (kRes) vr[i] = c < a.K8 ? reinterpret_cast<const uint4*>(a.residual)[base + c] : make_uint4(0, 0, 0, 0);
+    }
+    float h[V][8], sum = 0.f, mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      unpack8(vx[i], h[i]);
+      if (kRes) {
+        float r[8];
+        unpack8(vr[i], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+        const int c = i * NT + tid;
+        if (c < a.K8) reinterpret_cast<uint4*>(a.h)[base + c] = pack8(h[i]);
+      }
+      float wf[8];
+      unpack8(w[i], wf);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sum = fmaf(h[i][j], h[i][j], sum);
+        h[i][j] *= wf[j];
+        if (kFp8) mx = fmaxf(mx, fabsf(h[i][j]));
+      }
+    }
+    block_sum_max(sum, mx, red, parity);
+    const float f = norm_factor<kFp8>(a, row, sum, mx);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = i * NT + tid;
+      if (c >= a.K8) continue;
+      if (kFp8) {
+        reinterpret_cast<uint2*>(a.x8)[base + c] = codes8(h[i], f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] *= f;
+        reinterpret_cast<uint4*>(a.y)[base + c] = pack8(h[i]);
+      }
+    }
+  }
+}
+
+// Rows too long for the registers of one CTA: read twice (the second time
+// mostly from L2). A thread reads again only what it read itself, so h may
+// still be x or the residual.
+template <bool kRes, bool kFp8>
+__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
+  __shared__ float2 red[64];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
+    const int64_t base = row * a.K8;
+    float h[8], r[8], wf[8], sum = 0.f, mx = 0.f;
+    for (int c = threadIdx.x; c < a.K8; c += blockDim.x) {
+      unpack8(reinterpret_cast<const uint4*>(a.x)[base + c], h);
+      if (kRes) unpack8(reinterpret_cast<const uint4*>(a.residual)[base + c], r);
+      unpack8(reinterpret_cast<const uint4*>(a.w)[c], wf);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (kRes) h[j] += r[j];
+        sum = fmaf(h[j], h[j], sum);
+        mx = fmaxf(mx, fabsf(h[j] * wf[j]));
+      }
+    }
+    block_sum_max(sum, mx, red, parity);
+    const float f = norm_factor<kFp8>(a, row, sum, mx);
+    for (int c = threadIdx.x; c < a.K8; c += blockDim.x) {
+      unpack8(reinterpret_cast<const uint4*>(a.x)[base + c], h);
+      if (kRes) {
+        unpack8(reinterpret_cast<const uint4*>(a.residual)[base + c], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] += r[j];
+        reinterpret_cast<uint4*>(a.h)[base + c] = pack8(h);
+      }
+      unpack8(reinterpret_cast<const uint4*>(a.w)[c], wf);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] *= wf[j];
+      if (kFp8) {
+        reinterpret_cast<uint2*>(a.x8)[base + c] = codes8(h, f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] *= f;
+        reinterpret_cast<uint4*>(a.y)[base + c] = pack8(h);
+      }
+    }
+  }
+}
+
+struct SiluArgs {
+  const __half* gu;
+  __half* y;
+  uint8_t* x8;
+  float* sx;
+  int64_t M;
+  int F8;
+  int row_ctas;  // CTAs of a row (fp16 output)
+};
+
+__device__ __forceinline__ void silu8(const uint4& vg, const uint4& vu, float (&y)[8]) {
+  float u[8];
+  unpack8(vg, y);
+  unpack8(vu, u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = __fdividef(y[j], 1.f + ex2(-kLog2e * y[j])) * u[j];
+}
+
+// fp16 output: no reduction, a CTA takes blockDim * V vectors of one row.
+template <int V>
+__global__ void __launch_bounds__(256) silu_mul_kernel(const SiluArgs a) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t row = blockIdx.x / (unsigned)a.row_ctas;
+  const int c0 = (int)(blockIdx.x - row * a.row_ctas) * blockDim.x * V + threadIdx.x;
+  const uint4* g = reinterpret_cast<const uint4*>(a.gu) + row * 2 * a.F8;
+  uint4 vg[V], vu[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = c0 + i * blockDim.x;
+    if (c < a.F8) vg[i] = g[c], vu[i] = g[a.F8 + c];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = c0 + i * blockDim.x;
+    float y[8];
+    silu8(vg[i], vu[i], y);
+    if (c < a.F8) reinterpret_cast<uint4*>(a.y)[row * a.F8 + c] = pack8(y);
+  }
+}
+
+// Stores sx of a row whose largest |y| is mx and whose sum of y - y is `bad`
+// (0, or NaN when the row holds something that is not finite), and returns
+// the codes' factor 1 / sx. Below 2^-100 that factor would overflow fp32:
+// such a row counts as zero (a y below 2^-25 is zero in fp16 too).
+__device__ __forceinline__ float silu_factor(const SiluArgs& a, int64_t row, float bad, float mx) {
+  if (mx < 0x1p-100f) mx = 0.f;
+  if (threadIdx.x == 0) a.sx[row] = bad == 0.f ? mx * (1.f / kE4m3Max) : bad;
+  return mx > 0.f ? kE4m3Max / mx : 0.f;
+}
+
+// E4M3 output: one CTA a row at a time, the row in registers.
+template <int V>
+__global__ void __launch_bounds__(1024) silu_mul_fp8_kernel(const SiluArgs a) {
+  __shared__ float2 red[64];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int NT = blockDim.x, tid = threadIdx.x;
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
+    const uint4* g = reinterpret_cast<const uint4*>(a.gu) + row * 2 * a.F8;
+    float y[V][8], bad = 0.f, mx = 0.f;
+    uint4 vg[V], vu[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = i * NT + tid;
+      vg[i] = c < a.F8 ? g[c] : make_uint4(0, 0, 0, 0);
+      vu[i] = c < a.F8 ? g[a.F8 + c] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      silu8(vg[i], vu[i], y[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mx = fmaxf(mx, fabsf(y[i][j]));
+        bad += y[i][j] - y[i][j];
+      }
+    }
+    block_sum_max(bad, mx, red, parity);
+    const float f = silu_factor(a, row, bad, mx);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = i * NT + tid;
+      if (c < a.F8) reinterpret_cast<uint2*>(a.x8)[row * a.F8 + c] = codes8(y[i], f);
+    }
+  }
+}
+
+// E4M3 output of rows too long for the registers of one CTA: read twice.
+__global__ void __launch_bounds__(1024) silu_mul_fp8_long_kernel(const SiluArgs a) {
+  __shared__ float2 red[64];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
+    const uint4* g = reinterpret_cast<const uint4*>(a.gu) + row * 2 * a.F8;
+    float y[8], bad = 0.f, mx = 0.f;
+    for (int c = threadIdx.x; c < a.F8; c += blockDim.x) {
+      silu8(g[c], g[a.F8 + c], y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mx = fmaxf(mx, fabsf(y[j]));
+        bad += y[j] - y[j];
+      }
+    }
+    block_sum_max(bad, mx, red, parity);
+    const float f = silu_factor(a, row, bad, mx);
+    for (int c = threadIdx.x; c < a.F8; c += blockDim.x) {
+      silu8(g[c], g[a.F8 + c], y);
+      reinterpret_cast<uint2*>(a.x8)[row * a.F8 + c] = codes8(y, f);
+    }
+  }
+}
+
+// Threads of a CTA that holds a row of n vectors, V per thread.
+int row_threads(int n, int V) { return (n + 32 * V - 1) / (32 * V) * 32; }
+
+template <typename Args>
+cudaError_t launch_rows(void (*kernel)(Args), const Args& a, unsigned ctas, int threads, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// CTAs that walk M rows: as many as fit the SMs at once (2048 threads each).
+unsigned row_ctas(int64_t M, int threads) {
+  const int64_t fit = (int64_t)device_info().sm_count * (2048 / threads);
+  return (unsigned)(M < fit ? M : fit);
+}
+
+template <bool kRes, bool kFp8>
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
+  if (a.K8 > 4096) return launch_rows(rmsnorm_long_kernel<kRes, kFp8>, a, row_ctas(a.M, 1024), 1024, stream);
+  const int V = a.K8 <= 512 ? 1 : a.K8 <= 2048 ? 2 : 4;
+  const int t = row_threads(a.K8, V);
+  if (V == 1) return launch_rows(rmsnorm_kernel<1, kRes, kFp8>, a, row_ctas(a.M, t), t, stream);
+  if (V == 2) return launch_rows(rmsnorm_kernel<2, kRes, kFp8>, a, row_ctas(a.M, t), t, stream);
+  return launch_rows(rmsnorm_kernel<4, kRes, kFp8>, a, row_ctas(a.M, t), t, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm(const __half* x, const __half* residual, const __half* w, float eps, __half* h, __half* y,
+                           uint8_t* x8, float* sx, int64_t M, int64_t K, cudaStream_t stream) {
+  const NormArgs a{x, residual, w, h, y, x8, sx, eps, M, (int)(K / 8)};
+  if (residual) return x8 ? launch_norm<true, true>(a, stream) : launch_norm<true, false>(a, stream);
+  return x8 ? launch_norm<false, true>(a, stream) : launch_norm<false, false>(a, stream);
+}
+
+cudaError_t launch_silu_mul(const __half* gate_up, __half* y, uint8_t* x8, float* sx, int64_t M, int64_t F,
+                            cudaStream_t stream) {
+  SiluArgs a{gate_up, y, x8, sx, M, (int)(F / 8), 0};
+  if (x8) {
+    if (a.F8 > 4096) return launch_rows(silu_mul_fp8_long_kernel, a, row_ctas(M, 1024), 1024, stream);
+    const int V = a.F8 <= 512 ? 1 : a.F8 <= 2048 ? 2 : 4;
+    const int t = row_threads(a.F8, V);
+    if (V == 1) return launch_rows(silu_mul_fp8_kernel<1>, a, row_ctas(M, t), t, stream);
+    if (V == 2) return launch_rows(silu_mul_fp8_kernel<2>, a, row_ctas(M, t), t, stream);
+    return launch_rows(silu_mul_fp8_kernel<4>, a, row_ctas(M, t), t, stream);
+  }
+  constexpr int V = 2;
+  const int parts = (a.F8 + 256 * V - 1) / (256 * V);
+  const int t = row_threads((a.F8 + parts - 1) / parts, V);
+  a.row_ctas = (a.F8 + t * V - 1) / (t * V);
+  const int64_t ctas = M * a.row_ctas;
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_rows(silu_mul_kernel<V>, a, (unsigned)ctas, t, stream);
+}
+
+}  // namespace awq
