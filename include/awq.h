@@ -304,8 +304,8 @@ awq_status awq_silu_mul_fp8(const void* gate_up, void* x8, void* sx, int64_t M, 
  * status word. Bounds are clamped then, and tokens in such a block are not
  * written and read as zeros; nothing outside the buffers is touched.
  * Limits (AWQ_ERR_UNSUPPORTED): rows <= 2^24, seqs <= 2^20, seqs * heads <=
- * 2^24, q_heads <= 4096, rows * q_heads < 2^31, blocks < 2^31, table_width *
- * block_tokens <= 2^28. rows = 0 or seqs = 0 is a no-op.
+ * 2^24, q_heads <= 4096, rows * q_heads < 2^31, blocks * heads * block_tokens
+ * < 2^31, table_width * block_tokens <= 2^28. rows = 0 or seqs = 0 is a no-op.
  * q, k and v may be column ranges of one matrix: row r starts at element r *
  * stride, where the stride is a multiple of 8 and at least the row's width;
  * the heads of a row are contiguous. */

@@ -106,6 +106,7 @@ def test_kv8_shared_refusals(fn):
     for kw, code in ((dict(blocks=0), S), (dict(blocks=-1), S), (dict(heads=0), S), (dict(heads=-8), S),
                      (dict(head_dim=96), U), (dict(head_dim=256), U), (dict(block_tokens=8), U), (dict(block_tokens=48), U),
                      (dict(block_tokens=256), U), (dict(blocks=1 << 31), U),
+                     (dict(blocks=1 << 22), U),              # 2^31 rows of codes
                      (dict(k=None), I), (dict(v=None), I), (dict(k_exp=None), I), (dict(v_exp=None), I),
                      (dict(k=A + 8), P), (dict(v=B + 1), P),
                      (dict(v=A + 4096), I), (dict(k_exp=A), I), (dict(v_exp=C + 5), I)):

@@ -252,7 +252,7 @@ awq_status check_kv8(const awq_kv8_cache* cache, const awq_kv8_batch* batch, int
   if (cache->blocks < 0 || batch->table_width < 0) return AWQ_ERR_SHAPE;
   const int bs = cache->block_tokens;
   if (bs != 16 && bs != 32 && bs != 64 && bs != 128) return AWQ_ERR_UNSUPPORTED;
-  if (cache->blocks > 0x7FFFFFFF || batch->table_width > (int64_t(1) << 28) / bs) return AWQ_ERR_UNSUPPORTED;
+  if (cache->blocks > 0x7FFFFFFF || cache->blocks * cache->heads * bs > 0x7FFFFFFF || batch->table_width > (int64_t(1) << 28) / bs) return AWQ_ERR_UNSUPPORTED;
   *b = Kv8Batch{};
   if (batch->rows == 0 || batch->seqs == 0) return AWQ_OK;  // nothing is read or written: pointers may be null
   if (!cache->k || !cache->v || !cache->k_exp || !cache->v_exp || !batch->starts || !batch->lens || !batch->table || !workspace)

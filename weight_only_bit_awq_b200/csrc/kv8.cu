@@ -15,6 +15,14 @@
 #include "awq_internal.cuh"
 #include "sm100_ptx.cuh"
 
+#ifndef AT_S1
+#define AT_S1 2
+#define AT_S2 1
+#define AT_C1 2
+#define AT_C2 3
+#define AT_STAGES 3
+#endif
+
 namespace awq {
 namespace {
 
@@ -237,18 +245,27 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
 // operand. Codes become exact fp16 in registers; the products are exact, the
 // sums fp32.
 //
-// Bound by HBM: every code is read once, 4 flops a code and row. So each lane
-// copies exactly the codes that its own MMA fragments hold, 16 bytes at a
-// time with cp.async into its own part of a ring in shared memory: no
-// barrier, no bank conflict, no lane waits for another.
+// Bound by HBM: every code is read once, 4 flops a code and row. Each warp has
+// a ring of its own in shared memory, filled by TMA boxes of whole tokens that
+// its first lane asks for; warps never wait for one another within a segment.
+// The boxes are swizzled by 16-byte pieces, so that ldmatrix, which takes one
+// piece of 8 tokens at a time, has no bank conflicts. As 16-bit elements those
+// pieces are pairs of codes: for K, lane (g, t) gets channels 4t .. 4t + 3 of
+// token g, the A fragment of one k-step (the k order is free as long as q
+// follows it); for V, transposed, it gets channels 2g and 2g + 1 of tokens 2t
+// and 2t + 1, and one byte permutation makes them fragments.
 //
 // Softmax in one pass, in powers of two. With x = scale log2(e) q.k and the V
-// exponent e of a key's block, the weight kept for a key is
-// p = 2^(x + e - M + 15), M the running maximum of x + e: V's codes then need
-// no scaling, p uses fp16's range down to 2^-39 of the largest, and
-// l = sum p 2^-e is the denominator in the same unit. p is rounded to fp16
-// (2^-11 relative) for the second MMA; l sums the unrounded p.
-constexpr float kPOffset = 15.f;
+// exponent e of a key's block, the weight kept for a key is p = 2^(x + e - M):
+// V's codes then need no scaling, and l = sum p 2^-e is the denominator in the
+// same unit. Any M serves that keeps p within fp16. It follows the running
+// maximum of x + e, less kPOffset, but only when some exponent has grown past
+// kPMost: then p stays at most 2^15 (fp16 ends at 65504), the reduction over
+// lanes and the rescaling of O are skipped in most steps, and fp16's
+// subnormals begin 2^-26 below the largest weight. p is rounded to fp16 (2^-11
+// relative) for the second MMA; l sums the unrounded p.
+constexpr float kPOffset = 12.f, kPMost = 15.f;
+constexpr float kNoM = -1e30f;  // M of a row that has seen no key: far below any x, finite
 
 // The group of units that starts in a CTA's range and ends in a later one's.
 struct Kv8Fix {
@@ -264,41 +281,32 @@ struct AttnArgs {
   float* partial;     // [ctas][2][slot]
   int slot;           // floats of a slot: rows * (D + 2)
   Kv8Fix* fix;        // [ctas]
+  int cache_rows;     // blocks * heads * block_tokens
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// Copies that write zeros when !ok (then nothing is read).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+// Four 8 x 16-byte pieces: lane i gives the address of token i % 8 of piece i / 8.
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void ldsm4_trans(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
 }
 
 // D: head dimension; SUB: 16-key subtiles of a warp's step; NT: column tiles
@@ -308,25 +316,38 @@ template <int D, int SUB, int NT>
 struct Attn {
   static constexpr int kRows = 8 * NT;
   static constexpr int kKeys = kWarps * 16 * SUB;             // keys of a unit
-  static constexpr int kStages = 3;
-  static constexpr int kStageBytes = SUB * 32 * D;            // per warp: 16 keys, K and V
+  static constexpr int kStages = AT_STAGES;
+  static constexpr int kPartBytes = SUB * 16 * D;             // a warp's step of K, or of V
+  static constexpr int kStageBytes = 2 * kPartBytes;
   static constexpr int kMergeBytes = kWarps * kRows * (D + 4) * 4 + kWarps * kRows * 8;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+  static constexpr int kSmem = (kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes) + 1024;  // room to align
   static constexpr int kSlot = kRows * (D + 2);
-  static constexpr int kCtasPerSm = NT == 1 ? 4 : 3;          // 128 or 168 registers a thread
+  static constexpr int kCtasPerSm = NT == 1 ? AT_C1 : AT_C2;          // 128 or 168 registers a thread
 };
 
 template <int D, int SUB, int NT>
 __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
-    kv8_attention_kernel(const AttnArgs a, const Kv8Cache cache, const Kv8Batch bt, uint32_t* status) {
+    kv8_attention_kernel(const AttnArgs a, const Kv8Cache cache, const Kv8Batch bt,
+                         const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                         uint32_t* status) {
   using L = Attn<D, SUB, NT>;
   constexpr int KS = D / 16;     // k-steps of S
   constexpr int MT = D / 16;     // channel tiles of O
-  constexpr int KH = D / 64;     // 64-byte halves of a key
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ char smem_raw[];
+  char* const smem = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);  // the swizzle goes by address
   __shared__ int64_t scan[kWarps];
   __shared__ Place place;
+  __shared__ __align__(8) uint64_t full[kWarps * L::kStages];
+  __shared__ uint32_t abort_word;
+  volatile uint32_t* const abort_flag = &abort_word;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps * L::kStages; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
+    abort_word = 0;
+    ptx::fence_mbarrier_init();
+    ptx::prefetch_tensormap(&kmap);
+    ptx::prefetch_tensormap(&vmap);
+  }
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
 
@@ -349,7 +370,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
   const int64_t u1 = first_unit((int64_t)blockIdx.x + 1);
   Place p = find_item(bt.seqs, items, before, u, &place);
 
-  const uint32_t ring = ptx::smem_u32(smem) + warp * (L::kStages * L::kStageBytes) + lane * 16;
+  const uint32_t ring = ptx::smem_u32(smem) + warp * (L::kStages * L::kStageBytes);
+  const uint32_t bars = ptx::smem_u32(&full[warp * L::kStages]);
+  // The lane's row and piece of an ldmatrix: tokens (lane & 15), the first of
+  // two neighbouring pieces for lanes below 16; pieces are swizzled by token.
+  const uint32_t lrow = lane & 15, swz = D == 128 ? (lane & 7) : (lane >> 1 & 3);
+  const uint32_t lane_off = lrow * D + (((lane >> 4) ^ swz) << 4);
+  int stage = 0, fill = 0;   // ring positions of the next step to use and to fill
+  uint32_t parity = 0;
 
   while (u < u1) {
     Seq s = load_seq(bt, p.b, status);
@@ -368,16 +396,16 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
     const int rows = s.tokens * a.group, r0 = row_tile * L::kRows;
     const int past = s.len - s.tokens;
 
-    // ---- this segment's query rows as B fragments: k = channels of the lane's K bytes
+    // ---- this segment's query rows as B fragments, channels in K's order
     uint32_t qf[NT][KS][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = r0 + 8 * nt + g;
-      const __half* q = a.q + (int64_t)(s.row0 + r / a.group) * a.q_stride + ((int64_t)h * a.group + r % a.group) * D + 16 * t;
+      const __half* q = a.q + (int64_t)(s.row0 + r / a.group) * a.q_stride + ((int64_t)h * a.group + r % a.group) * D + 4 * t;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint2 v = make_uint2(0, 0);
-        if (r < rows) v = *reinterpret_cast<const uint2*>(q + 64 * (ks / 4) + 4 * (ks % 4));
+        if (r < rows) v = *reinterpret_cast<const uint2*>(q + 16 * ks);
         qf[nt][ks][0] = v.x;
         qf[nt][ks][1] = v.y;
       }
@@ -386,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) limit[nt][c] = past + (r0 + 8 * nt + 2 * t + c) / a.group + 1;
+      for (int c = 0; c < 2; ++c) limit[nt][c] = min(past + (r0 + 8 * nt + 2 * t + c) / a.group + 1, s.len);
     const int least = past + r0 / a.group + 1;  // keys that every row sees
 
     float o[NT][MT][4], M[NT][2], l[NT][2];
@@ -394,13 +422,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      M[nt][0] = M[nt][1] = -INFINITY;
+      M[nt][0] = M[nt][1] = kNoM;
       l[nt][0] = l[nt][1] = 0.f;
     }
 
     // Blocks and exponents of the next 32 subtiles of this warp, one per lane.
     const int* table = bt.table + (int64_t)p.b * bt.table_width;
-    auto key_of = [&](int sub) { return (tile0 + sub / SUB) * L::kKeys + warp * 16 * SUB + (sub % SUB) * 16; };
+    const int key00 = tile0 * L::kKeys + warp * 16 * SUB;
+    auto key_of = [&](int sub) { return key00 + sub / SUB * L::kKeys + (sub % SUB) * 16; };
     int blk = -1, exps = 0, exps_prev = 0;
     auto load_info = [&](int sub0) {
       const int sub = sub0 + lane, key = key_of(sub);
@@ -418,109 +447,105 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
         }
       }
     };
+    // Steps with keys of this warp, and the boxes that bring them: min(block,
+    // step) tokens each. A box of a block that is not there starts behind the
+    // cache's last row, which reads as zeros.
+    const int steps = s.len > key00 ? min((s.len - key00 + L::kKeys - 1) / L::kKeys, n) : 0;
+    const int box = min(bs, 16 * SUB);
     auto issue = [&](int step) {
-      if (step < n) {
-        if ((step * SUB) % 32 == 0) load_info(step * SUB);
-        const uint32_t dst = ring + (step % L::kStages) * L::kStageBytes;
-#pragma unroll
-        for (int sb = 0; sb < SUB; ++sb) {
-          const int sub = step * SUB + sb, key = key_of(sub);
-          const int id = __shfl_sync(0xffffffffu, blk, sub & 31);
-          const int64_t at = (((int64_t)max(id, 0) * cache.heads + h) * bs + (key & (bs - 1))) * D;
-          const int live = id < 0 ? 0 : s.len - key;  // keys of the subtile that exist
-          const uint32_t d0 = dst + sb * (32 * D);
-#pragma unroll
-          for (int rh = 0; rh < 2; ++rh)
-#pragma unroll
-            for (int kh = 0; kh < KH; ++kh) {
-              const bool ok = 8 * rh + g < live;
-              copy16(d0 + (rh * KH + kh) * 512, cache.k + at + (ok ? (8 * rh + g) * D : 0) + 64 * kh + 16 * t, ok);
-            }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const int kn = 2 * t + (kk & 1) + 8 * (kk >> 1);
-            const bool ok = kn < live;
-            if (D == 128)
-              copy16(d0 + 16 * D + kk * 512, cache.v + at + (ok ? kn * D : 0) + 16 * g, ok);
-            else
-              copy8(d0 + 16 * D + (kk >> 1) * 512 + (kk & 1) * 8, cache.v + at + (ok ? kn * D : 0) + 8 * g, ok);
-          }
+      if (step >= steps) return;
+      if ((step * SUB) % 32 == 0) load_info(step * SUB);
+      const uint32_t bar = bars + 8 * fill, dst = ring + fill * L::kStageBytes;
+      fill = fill == L::kStages - 1 ? 0 : fill + 1;
+      __syncwarp();  // every lane has read what the stage held
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
+      for (int i = 0; i < 16 * SUB; i += box) {
+        const int id = __shfl_sync(0xffffffffu, blk, step * SUB + i / 16);
+        const int row = id < 0 ? a.cache_rows : (id * cache.heads + h) * bs + ((key00 + step * L::kKeys + i) & (bs - 1));
+        if (lane == 0) {
+          ptx::tma_load_2d(dst + i * D, &kmap, 0, row, bar);
+          ptx::tma_load_2d(dst + L::kPartBytes + i * D, &vmap, 0, row, bar);
         }
       }
-      copy_commit();
     };
 
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < L::kStages - 1; ++i) issue(i);
-    for (int step = 0; step < n; ++step) {
+    for (int step = 0; step < steps; ++step) {
       issue(step + L::kStages - 1);
-      copy_wait<L::kStages - 1>();
-      const uint32_t src = ring + (step % L::kStages) * L::kStageBytes;
+      ptx::wait_bar(bars + 8 * stage, parity, abort_flag, status);  // on a timeout the rest is garbage, soon over
+      __syncwarp();
+      const uint32_t src = ring + stage * L::kStageBytes + lane_off;
+      stage = stage == L::kStages - 1 ? 0 : stage + 1;
+      parity ^= stage == 0;
+      const int key0 = key00 + step * L::kKeys;
+      // the issuing side is up to kStages - 1 steps ahead: it may have loaded the next 32 already
+      const int e_of = (step * SUB) / 32 == min(step + L::kStages - 1, steps - 1) * SUB / 32 ? exps : exps_prev;
 
-      // S^T of the step's subtiles, as x + e_v (masked keys: -inf)
-      float x[SUB][NT][4], inv_ev[SUB];
+      // x + e_v of the step's keys (masked keys: -inf)
+      float x[SUB][NT][4], unit[SUB];  // unit: 2^-e_v
 #pragma unroll
-      for (int sb = 0; sb < SUB; ++sb) {
-        uint4 kw[2][KH];
-#pragma unroll
-        for (int rh = 0; rh < 2; ++rh)
-#pragma unroll
-          for (int kh = 0; kh < KH; ++kh) kw[rh][kh] = lds16(src + sb * (32 * D) + (rh * KH + kh) * 512);
+      for (int sb = 0; sb < SUB; ++sb)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) x[sb][nt][0] = x[sb][nt][1] = x[sb][nt][2] = x[sb][nt][3] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint4 &ka = kw[0][ks / 4], &kb = kw[1][ks / 4];
-          const uint32_t wa = ks % 4 == 0 ? ka.x : ks % 4 == 1 ? ka.y : ks % 4 == 2 ? ka.z : ka.w;
-          const uint32_t wb = ks % 4 == 0 ? kb.x : ks % 4 == 1 ? kb.y : ks % 4 == 2 ? kb.z : kb.w;
-          const uint32_t a0 = lo_h2(wa), a1 = lo_h2(wb), a2 = hi_h2(wa), a3 = hi_h2(wb);
+      for (int ks = 0; ks < KS; ks += 2)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(x[sb][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+        for (int sb = 0; sb < SUB; ++sb) {
+          uint32_t w[4];  // tokens g and g + 8 of piece ks, then of ks + 1
+          ldsm4((src + sb * (16 * D)) ^ (ks << 4), w);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a0 = lo_h2(w[2 * i]), a1 = lo_h2(w[2 * i + 1]), a2 = hi_h2(w[2 * i]), a3 = hi_h2(w[2 * i + 1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(x[sb][nt], a0, a1, a2, a3, qf[nt][ks + i][0], qf[nt][ks + i][1]);
+          }
         }
-        const int sub = step * SUB + sb, key = key_of(sub);
-        // the issuing side is up to kStages - 1 steps ahead: it may have loaded the next 32 already
-        const int ahead = min(step + L::kStages - 1, n - 1) * SUB / 32;
-        const int e2 = __shfl_sync(0xffffffffu, sub / 32 == ahead ? exps : exps_prev, sub & 31);
-        const float ks2 = a.scale_log2 * __int_as_float(((int)(int8_t)e2 + 127) << 23);
-        const int ev = (int8_t)(e2 >> 8);
-        inv_ev[sb] = __int_as_float((127 - ev) << 23);
+#pragma unroll
+      for (int sb = 0; sb < SUB; ++sb) {
+        const int e2 = __shfl_sync(0xffffffffu, e_of, step * SUB + sb);
+        const float k_unit = a.scale_log2 * __int_as_float(((int)(int8_t)e2 + 127) << 23);
+        const int ev = (int)(e2 << 16) >> 24;
+        unit[sb] = __int_as_float((127 - ev) << 23);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[sb][nt][c] = fmaf(x[sb][nt][c], ks2, (float)ev);
-        if (key + 16 > least) {
+          for (int c = 0; c < 4; ++c) x[sb][nt][c] = fmaf(x[sb][nt][c], k_unit, (float)ev);
+      }
+      if (key0 + 16 * SUB > least) {  // some row does not see all of the step's keys
+#pragma unroll
+        for (int sb = 0; sb < SUB; ++sb)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (key + g + 8 * (c >> 1) >= min(limit[nt][c & 1], s.len)) x[sb][nt][c] = -INFINITY;
-        }
+              if (key0 + 16 * sb + g + 8 * (c >> 1) >= limit[nt][c & 1]) x[sb][nt][c] = -INFINITY;
       }
 
-      // running maximum over keys (rows of S^T: the lanes' g)
-      float Mn[NT][2];
-      bool grew = false;
+      // Where a weight's exponent x - M exceeds kPMost (or a row has no M yet),
+      // every row's M follows its running maximum.
+      float over = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int sb = 0; sb < SUB; ++sb)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m = M[nt][c];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int sb = 0; sb < SUB; ++sb) m = fmaxf(m, fmaxf(x[sb][nt][c], x[sb][nt][c + 2]));
-#pragma unroll
-          for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-          Mn[nt][c] = m;
-          grew |= m > M[nt][c];
-        }
-      if (__any_sync(0xffffffffu, grew)) {
+          for (int c = 0; c < 4; ++c) over = fmaxf(over, x[sb][nt][c] - M[nt][c & 1]);
+      if (__any_sync(0xffffffffu, over > kPMost)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float f[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            f[c] = Mn[nt][c] == -INFINITY ? 0.f : ex2(M[nt][c] - Mn[nt][c]);
+            float m = -INFINITY;
+#pragma unroll
+            for (int sb = 0; sb < SUB; ++sb) m = fmaxf(m, fmaxf(x[sb][nt][c], x[sb][nt][c + 2]));
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+            m = fmaxf(M[nt][c], m - kPOffset);
+            f[c] = ex2(M[nt][c] - m);
             l[nt][c] *= f[c];
-            M[nt][c] = Mn[nt][c];
+            M[nt][c] = m;
           }
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
@@ -530,79 +555,69 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
         }
       }
 
+      uint32_t pf[SUB][NT][2];
 #pragma unroll
-      for (int sb = 0; sb < SUB; ++sb) {
-        uint32_t pf[NT][2];
+      for (int sb = 0; sb < SUB; ++sb)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float pr[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float m = M[nt][c & 1] == -INFINITY ? 0.f : M[nt][c & 1];
-            pr[c] = ex2(x[sb][nt][c] - m + kPOffset);
-            l[nt][c & 1] = fmaf(pr[c], inv_ev[sb], l[nt][c & 1]);
-          }
-          pf[nt][0] = transpose8x8(f2h(pr[0], pr[1]));
-          pf[nt][1] = transpose8x8(f2h(pr[2], pr[3]));
+          for (int c = 0; c < 4; ++c) pr[c] = ex2(x[sb][nt][c] - M[nt][c & 1]);
+          l[nt][0] = fmaf(pr[0] + pr[2], unit[sb], l[nt][0]);
+          l[nt][1] = fmaf(pr[1] + pr[3], unit[sb], l[nt][1]);
+          pf[sb][nt][0] = transpose8x8(f2h(pr[0], pr[1]));
+          pf[sb][nt][1] = transpose8x8(f2h(pr[2], pr[3]));
         }
-        const uint32_t vsrc = src + sb * (32 * D) + 16 * D;
-        uint32_t vw[4][MT / 2];  // the lane's channels of keys 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (D == 128) {
-            const uint4 v = lds16(vsrc + kk * 512);
-            vw[kk][0] = v.x, vw[kk][1] = v.y, vw[kk][MT / 2 - 2] = v.z, vw[kk][MT / 2 - 1] = v.w;
-          } else {
-            const uint2 v = lds8(vsrc + (kk >> 1) * 512 + (kk & 1) * 8);
-            vw[kk][0] = v.x, vw[kk][1] = v.y;
-          }
-        }
-        // Where some rows do not see all 16 keys, a NaN code must reach only
-        // the rows that see it: 0 * NaN in the MMA would reach all. Such codes
-        // are taken out and their channels of the rows that see them set to NaN here.
-        const int key = key_of(step * SUB + sb);
-        if (least < s.len && key + 16 > least) {
-          uint32_t nan[4][MT / 2], any = 0;
+      for (int sb = 0; sb < SUB; ++sb) {
+        const int key = key0 + 16 * sb;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
+        for (int i = 0; i < MT; i += 2) {
+          uint32_t w[4];  // channels 2g, 2g + 1 of piece i: tokens 2t, 2t + 1, then + 8; the same of piece i + 1
+          ldsm4_trans((src + L::kPartBytes + sb * (16 * D)) ^ (i << 4), w);
+          // Where a row does not see all 16 keys, a NaN code must reach only
+          // the rows that see it: 0 * NaN in the MMA would reach all. Such
+          // codes are taken out, and their channels of the rows that see them
+          // set to NaN here. (Places behind the end can hold NaN codes too.)
+          if (key + 16 > least) {
+            uint32_t nan[4], any = 0;
 #pragma unroll
-            for (int w = 0; w < MT / 2; ++w) {
-              nan[kk][w] = ((vw[kk][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // 0x80 in bytes that are 0x7F or 0xFF
-              any |= nan[kk][w];
+            for (int j = 0; j < 4; ++j) {
+              nan[j] = ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // 0x80 in bytes that are 0x7F or 0xFF
+              any |= nan[j];
             }
-          if (__any_sync(0xffffffffu, any)) {
+            if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-              for (int w = 0; w < MT / 2; ++w) {
-                vw[kk][w] &= ~((nan[kk][w] >> 7) * 0xFFu);
+              for (int j = 0; j < 4; ++j) {
+                w[j] &= ~((nan[j] >> 7) * 0xFFu);
 #pragma unroll 1
                 for (int tt = 0; tt < 4; ++tt) {  // the four lanes that share this lane's channels
-                  const uint32_t m = __shfl_sync(0xffffffffu, nan[kk][w], (lane & ~3) | tt);
-                  const int at = key + 2 * tt + (kk & 1) + 8 * (kk >> 1);
+                  const uint32_t m = __shfl_sync(0xffffffffu, nan[j], (lane & ~3) | tt);
+                  if (m == 0) continue;
 #pragma unroll
                   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
+                    for (int b = 0; b < 4; ++b)  // byte b: token + (b >> 1), channel + (b & 1)
 #pragma unroll
                       for (int c = 0; c < 2; ++c)
-                        if ((m >> (8 * b + 7) & 1) && at < limit[nt][c]) o[nt][2 * w + (b >> 1)][2 * (b & 1) + c] = NAN;
+                        if ((m >> (8 * b + 7) & 1) && key + 2 * tt + 8 * (j & 1) + (b >> 1) < limit[nt][c])
+                          o[nt][i + (j >> 1)][2 * (b & 1) + c] = NAN;
                 }
               }
+            }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
-          const uint32_t p01 = __byte_perm(vw[0][i / 2], vw[1][i / 2], sel);
-          const uint32_t p23 = __byte_perm(vw[2][i / 2], vw[3][i / 2], sel);
-          const uint32_t a0 = lo_h2(p01), a1 = hi_h2(p01), a2 = lo_h2(p23), a3 = hi_h2(p23);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t p0 = __byte_perm(w[2 * j], 0, 0x3120), p1 = __byte_perm(w[2 * j + 1], 0, 0x3120);
+            const uint32_t a0 = lo_h2(p0), a1 = hi_h2(p0), a2 = lo_h2(p1), a3 = hi_h2(p1);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i + j], a0, a1, a2, a3, pf[sb][nt][0], pf[sb][nt][1]);
+          }
         }
       }
     }
-    copy_wait<0>();
+    if (*abort_flag)  // a wait gave up: no copy may land after this CTA is gone
+      for (int i = 0; i < L::kStages; ++i) ptx::drain_bar(bars + 8 * i, i < stage ? parity : parity ^ 1);
 
     // ---- the four warps' parts of the segment
 #pragma unroll
@@ -621,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
         const int r = warp * L::kRows + 8 * nt + 2 * t + c;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-          *reinterpret_cast<float2*>(mo + r * (D + 4) + (D / 8) * g + 2 * i) = make_float2(o[nt][i][c], o[nt][i][c + 2]);
+          *reinterpret_cast<float2*>(mo + r * (D + 4) + 16 * i + 2 * g) = make_float2(o[nt][i][c], o[nt][i][c + 2]);
         if (g == 0) ml[r] = make_float2(M[nt][c], l[nt][c]);
       }
     __syncthreads();
@@ -630,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
     for (int i = tid; i < L::kRows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
       if (r0 + r >= rows) continue;
-      float mx = -INFINITY;
+      float mx = kNoM;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml[w * L::kRows + r].x);
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -638,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 v = ml[w * L::kRows + r];
-        const float f = v.x == -INFINITY && v.y == 0.f ? 0.f : ex2(v.x - (mx == -INFINITY ? 0.f : mx));
+        const float f = ex2(v.x - mx);
         const float4 ow = *reinterpret_cast<const float4*>(mo + (w * L::kRows + r) * (D + 4) + d);
         sum.x = fmaf(f, ow.x, sum.x), sum.y = fmaf(f, ow.y, sum.y);
         sum.z = fmaf(f, ow.z, sum.z), sum.w = fmaf(f, ow.w, sum.w);
@@ -659,51 +674,76 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
       a.fix[blockIdx.x] = Kv8Fix{1, s.row0, rows, r0, h, (int)((end * ctas + total - 1) / total) - 1, 0, 0};
     }
     u += n;
-    __syncthreads();  // the merge buffer is the next segment's ring
+    ptx::fence_proxy_async_smem();  // the merge buffer is the next segment's ring
+    if (__syncthreads_or(*abort_flag)) break;
   }
 }
 
-// Adds the parts of the groups that more than one CTA worked on, in CTA order
-// (so the result does not depend on timing). CTA c of this kernel has the
-// group that starts in CTA c of the attention kernel: one part in that CTA's
-// slot 1, the others in the following CTAs' slots 0. A warp takes a row.
-template <int D>
-__global__ void __launch_bounds__(256) kv8_fixup_kernel(const AttnArgs a, int heads, int tile_rows) {
+// Adds the parts of the groups that more than one CTA worked on, in a fixed
+// order (so the result does not depend on timing). CTA (c, .) has the group
+// that starts in CTA c of the attention kernel: one part in that CTA's slot 1,
+// the others in the following CTAs' slots 0. Few groups have many parts each
+// (long sequences): kSplit gives a CTA one row, its warps every fourth part.
+// Many groups have few parts: then a warp takes a row.
+template <int D, bool kSplit>
+__global__ void __launch_bounds__(kThreads) kv8_fixup_kernel(const AttnArgs a, int heads, int tile_rows) {
+  __shared__ float2 wml[kWarps];
+  __shared__ float wsum[kWarps][D];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const Kv8Fix f = a.fix[blockIdx.x];
-  if (!f.valid) return;
-  const int lane = threadIdx.x & 31, parts = f.last_cta - (int)blockIdx.x + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = kSplit ? (int)blockIdx.y : (int)blockIdx.y * kWarps + warp;
+  if (!f.valid || f.tile0 + r >= f.rows) return;
+  const int parts = f.last_cta - (int)blockIdx.x + 1;
   constexpr int E = D / 32;  // channels per lane
-  auto part = [&](int i) {
-    return a.partial + (((int64_t)blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * a.slot;
-  };
-  for (int r = threadIdx.x >> 5; r < tile_rows && f.tile0 + r < f.rows; r += 8) {
-    float mx = -INFINITY;
-    for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, part(i)[tile_rows * D + 2 * r]);
+  auto part = [&](int i) { return a.partial + (((int64_t)blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * a.slot; };
+  const int first = kSplit ? warp : 0, by = kSplit ? kWarps : 1;
+  float mx = kNoM;
+  for (int i = first + by * lane; i < parts; i += 32 * by) mx = fmaxf(mx, part(i)[tile_rows * D + 2 * r]);
 #pragma unroll
-    for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    const float m0 = mx == -INFINITY ? 0.f : mx;
-    float sum[E] = {}, den = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const float* pt = part(i);
-      const float2 v = *reinterpret_cast<const float2*>(pt + tile_rows * D + 2 * r);
-      const float w = v.x == -INFINITY && v.y == 0.f ? 0.f : ex2(v.x - m0);
-      den = fmaf(w, v.y, den);
+  for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+  float sum[E] = {}, den = 0.f;
+#pragma unroll 8
+  for (int i = first; i < parts; i += by) {
+    const float* pt = part(i);
+    const float2 v = *reinterpret_cast<const float2*>(pt + tile_rows * D + 2 * r);
+    const float w = ex2(v.x - mx);
+    den = fmaf(w, v.y, den);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(pt + r * D + 32 * e + 2 * lane);
+      sum[e] = fmaf(w, x.x, sum[e]);
+      sum[e + 1] = fmaf(w, x.y, sum[e + 1]);
+    }
+  }
+  if (kSplit) {
+    if (lane == 0) wml[warp] = make_float2(mx, den);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(&wsum[warp][32 * e + 2 * lane]) = make_float2(sum[e], sum[e + 1]);
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, wml[w].x);
+    den = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float k = ex2(wml[w].x - mx);
+      den = fmaf(k, wml[w].y, den);
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(pt + r * D + 64 * (e / 2) + 2 * lane);
-        sum[e] = fmaf(w, x.x, sum[e]);
-        sum[e + 1] = fmaf(w, x.y, sum[e + 1]);
+        sum[e] = fmaf(k, wsum[w][32 * e + 2 * lane], sum[e]);
+        sum[e + 1] = fmaf(k, wsum[w][32 * e + 2 * lane + 1], sum[e + 1]);
       }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    const int64_t at = (int64_t)(f.row0 + (f.tile0 + r) / a.group) * heads * a.group + (int64_t)f.head * a.group + (f.tile0 + r) % a.group;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(a.out + at * D + 64 * (e / 2) + 2 * lane) = f2h(sum[e] * inv, sum[e + 1] * inv);
   }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const int64_t at = (int64_t)(f.row0 + (f.tile0 + r) / a.group) * heads * a.group + (int64_t)f.head * a.group + (f.tile0 + r) % a.group;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(a.out + at * D + 32 * e + 2 * lane) = f2h(sum[e] * inv, sum[e + 1] * inv);
 }
 
 template <typename... P, typename... A>
@@ -736,11 +776,29 @@ cudaError_t launch_attention(AttnArgs a, const Kv8Cache& cache, const Kv8Batch& 
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(uint64_t(1) << dev, std::memory_order_acq_rel);
   }
+  CUtensorMap maps[2];
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)a.cache_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)D};
+    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)(bt.block_tokens < 16 * SUB ? bt.block_tokens : 16 * SUB)};
+    const cuuint32_t estr[2] = {1, 1};
+    auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, i ? cache.v : cache.k, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
   a.slot = L::kSlot;
   const int ctas = L::kCtasPerSm * device_info().sm_count;  // all resident: a persistent grid
-  cudaError_t e = launch_pdl(kv8_attention_kernel<D, SUB, NT>, dim3((unsigned)ctas), kThreads, L::kSmem, stream, a, cache, bt, status);
+  cudaError_t e = launch_pdl(kv8_attention_kernel<D, SUB, NT>, dim3((unsigned)ctas), kThreads, L::kSmem, stream, a, cache, bt, maps[0], maps[1], status);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_fixup_kernel<D>, dim3((unsigned)ctas), 256, 0, stream, a, cache.heads, L::kRows);
+  // groups of units at most; with eight or more parts each, a CTA per row
+  const int64_t groups = (int64_t)cache.heads * (bt.seqs + (int64_t)bt.rows * a.group / L::kRows);
+  if (groups * 8 <= ctas)
+    return launch_pdl(kv8_fixup_kernel<D, true>, dim3((unsigned)ctas, L::kRows), kThreads, 0, stream, a, cache.heads, L::kRows);
+  return launch_pdl(kv8_fixup_kernel<D, false>, dim3((unsigned)ctas, L::kRows / kWarps), kThreads, 0, stream, a, cache.heads,
+                    L::kRows);
 }
 
 }  // namespace
@@ -777,16 +835,17 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
   a.out = out;
   a.group = q_heads / cache.heads;
   a.scale_log2 = scale * kLog2e;
+  a.cache_rows = (int)(cache.blocks * cache.heads * bt.block_tokens);
   a.fix = reinterpret_cast<Kv8Fix*>(ws + kWsHeaderBytes);
   a.partial = reinterpret_cast<float*>(ws + kWsHeaderBytes + ctas * sizeof(Kv8Fix));
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
   // rows that share a kv head, by the mean of new tokens a sequence (lengths are on the device)
   const int64_t rows = ((int64_t)bt.rows + bt.seqs - 1) / bt.seqs * a.group;
   if (cache.head_dim == 128)
-    return rows <= 8 ? launch_attention<128, 1, 1>(a, cache, bt, status, stream)
-                     : launch_attention<128, 1, 2>(a, cache, bt, status, stream);
-  return rows <= 8 ? launch_attention<64, 2, 1>(a, cache, bt, status, stream)
-                   : launch_attention<64, 2, 2>(a, cache, bt, status, stream);
+    return rows <= 8 ? launch_attention<128, AT_S1, 1>(a, cache, bt, status, stream)
+                     : launch_attention<128, AT_S2, 2>(a, cache, bt, status, stream);
+  return rows <= 8 ? launch_attention<64, 2*AT_S1, 1>(a, cache, bt, status, stream)
+                   : launch_attention<64, 2*AT_S2, 2>(a, cache, bt, status, stream);
 }
 
 }  // namespace awq
