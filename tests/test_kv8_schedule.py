@@ -1,13 +1,17 @@
 """Host model of the cache attention's work split (csrc/kv8.cu): units of
-64 keys (128 for 64-wide heads) of one (sequence, kv head, row tile), equal
-contiguous ranges of them per CTA, and the hand-over of groups that several
-CTAs work on to the fixup kernel. Checked on random ragged batches: every unit
+128 keys (256 for 64-wide heads) of one group (sequence, kv head, row tile),
+behind two units per group that stand for its fixed cost and hold no keys;
+equal contiguous ranges of them per CTA; and the hand-over of groups that
+several CTAs work on to the fixup kernel. Checked on random ragged batches: every unit
 is computed once, a group's rows are written once, by the CTA that computes
 all of it or by the fixup, and the fixup reads exactly the slots that the
 group's contributors wrote."""
 import random
 
 import pytest
+
+
+COST = 2   # units of a group that hold no keys
 
 
 def plan(seqs, group, heads, rows_per_tile, keys_per_unit):
@@ -17,9 +21,9 @@ def plan(seqs, group, heads, rows_per_tile, keys_per_unit):
 
 def simulate(seqs, group, heads, rows_per_tile, keys_per_unit, grid):
     tiles = plan(seqs, group, heads, rows_per_tile, keys_per_unit)
-    total = sum(r * k * heads for r, k in tiles)
+    total = sum(r * (k + COST) * heads for r, k in tiles)
     ctas = min(total, grid)
-    owner = {}      # unit -> CTA
+    owner = {}      # (group, key tile) -> CTA
     direct = set()  # groups written by the attention kernel
     slots = {}      # (cta, slot) -> group
     fix = {}        # cta -> (group, last cta)
@@ -28,19 +32,24 @@ def simulate(seqs, group, heads, rows_per_tile, keys_per_unit, grid):
         u1 = total // ctas * (c + 1) + total % ctas * (c + 1) // ctas
         b, base = 0, 0
         while u < u1:
-            while u >= base + tiles[b][0] * tiles[b][1] * heads:
-                base += tiles[b][0] * tiles[b][1] * heads
+            while u >= base + tiles[b][0] * (tiles[b][1] + COST) * heads:
+                base += tiles[b][0] * (tiles[b][1] + COST) * heads
                 b += 1
             rt, kt = tiles[b]
-            g, tile0 = divmod(u - base, kt)
+            g, v0 = divmod(u - base, kt + COST)
+            take = min(u1 - u, kt + COST - v0)
+            tile0 = max(v0 - COST, 0)
+            n = v0 + take - COST - tile0
+            u += take
+            if n <= 0:
+                continue
             h, row_tile = divmod(g, rt)
-            n = min(u1 - u, kt - tile0)
-            for i in range(n):
-                assert u + i not in owner
-                owner[u + i] = c
             who = (b, h, row_tile)
             assert 0 <= h < heads and 0 <= row_tile < rt
-            if tile0 == 0 and n == kt:
+            for i in range(tile0, tile0 + n):
+                assert (who, i) not in owner and i < kt
+                owner[who, i] = c
+            if tile0 == 0 and v0 + take == kt + COST:
                 assert who not in direct
                 direct.add(who)
             else:
@@ -48,11 +57,10 @@ def simulate(seqs, group, heads, rows_per_tile, keys_per_unit, grid):
                 assert key not in slots
                 slots[key] = who
                 if tile0 == 0:
-                    end = u + kt
+                    end = base + (g + 1) * (kt + COST)
                     assert c not in fix
                     fix[c] = (who, (end * ctas + total - 1) // total - 1)
-            u += n
-    assert sorted(owner) == list(range(total))
+    assert len(owner) == sum(r * k * heads for r, k in tiles)
     fixed = set()
     for c, (who, last) in fix.items():
         assert last > c
@@ -72,11 +80,11 @@ def test_every_unit_once_and_every_group_written_once(seed):
         B = rng.randint(1, 20)
         seqs = [(rng.choice([0, 1, 1, 1, rng.randint(2, 40)]), rng.choice([0, 1, rng.randint(1, 300), rng.randint(1, 9000)]))
                 for _ in range(B)]
-        simulate(seqs, rng.choice([1, 4, 8, 29]), rng.choice([1, 2, 8]), rng.choice([8, 16]), rng.choice([64, 128]),
-                 rng.choice([1, 3, 148, 444, 592]))
+        simulate(seqs, rng.choice([1, 4, 8, 29]), rng.choice([1, 2, 8]), rng.choice([8, 16]), rng.choice([128, 256]),
+                 rng.choice([1, 3, 148, 296]))
 
 
 def test_long_and_empty_batches():
-    simulate([(1, 131072)], 4, 8, 8, 64, 592)
-    simulate([(0, 0), (0, 50), (1, 0)], 4, 8, 8, 64, 592)
-    simulate([(0, 0)], 4, 8, 8, 64, 592)
+    simulate([(1, 131072)], 4, 8, 8, 128, 296)
+    simulate([(0, 0), (0, 50), (1, 0)], 4, 8, 8, 128, 296)
+    simulate([(0, 0)], 4, 8, 8, 128, 296)

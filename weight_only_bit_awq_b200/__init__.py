@@ -291,25 +291,31 @@ def awq_w4a8_gemm(x8, sx, qweight, scales, zeros, row_exp, N, workspace, group: 
     return y
 
 
+# The current device and the raw handle of its current stream, without the
+# Python objects around them (2 us a call) where torch has the short way.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _call(fn, name: str, tensors, *args):
     """fn(*args, stream) on the device of the tensors (which must share one),
     on that device's current stream."""
-    device = tensors[0].device
+    device = tensors[0].get_device()
     for t in tensors:
-        if t.device != device:
-            raise ValueError(f"{name}: tensors on {device} and {t.device}")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), name)
+        if t.get_device() != device:
+            raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
+    if device == _current_device():
+        status = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), name)
+            status = fn(*args, _raw_stream(device))
+    if status != 0:
+        raise AwqError(status, name)
 
 
-def _out(t, shape, dtype, name: str, device) -> torch.Tensor:
-    """The output `t`, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != shape:
+def _given(t, shape, dtype, name: str) -> torch.Tensor:
+    """The caller's output `t`, checked."""
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
     _dev(t, dtype, name)
     return t
@@ -328,7 +334,7 @@ def _norm_inputs(x, weight, residual, h):
     pr = _dev(residual, torch.float16, "residual")
     if residual.shape != (M, K):
         raise ValueError(f"residual must be [{M}, {K}]")
-    h = _out(h, (M, K), torch.float16, "h", x.device)
+    h = torch.empty_like(x) if h is None else _given(h, (M, K), torch.float16, "h")
     return M, K, tensors + [residual, h], px, pr, pw, h
 
 
@@ -337,7 +343,7 @@ def awq_rmsnorm(x, weight, eps: float, residual=None, h=None, y=None):
     residual n = x + residual; then (y, h) is returned, h = n rounded to fp16
     (h may be x or residual itself: updated in place)."""
     M, K, tensors, px, pr, pw, h = _norm_inputs(x, weight, residual, h)
-    y = _out(y, (M, K), torch.float16, "y", x.device)
+    y = torch.empty_like(x) if y is None else _given(y, (M, K), torch.float16, "y")
     _call(lib.awq_rmsnorm, "awq_rmsnorm", tensors + [y], px, pr, pw, eps, None if h is None else h.data_ptr(),
           y.data_ptr(), M, K)
     return y if h is None else (y, h)
@@ -347,8 +353,8 @@ def awq_rmsnorm_fp8(x, weight, eps: float, residual=None, h=None, x8=None, sx=No
     """awq_rmsnorm with y as (x8 uint8 E4M3 codes [M][K], sx float32 [M]), the
     inputs of awq_w4a8_gemm; (x8, sx, h) with a residual."""
     M, K, tensors, px, pr, pw, h = _norm_inputs(x, weight, residual, h)
-    x8 = _out(x8, (M, K), torch.uint8, "x8", x.device)
-    sx = _out(sx, (M,), torch.float32, "sx", x.device)
+    x8 = x.new_empty((M, K), dtype=torch.uint8) if x8 is None else _given(x8, (M, K), torch.uint8, "x8")
+    sx = x.new_empty(M, dtype=torch.float32) if sx is None else _given(sx, (M,), torch.float32, "sx")
     _call(lib.awq_rmsnorm_fp8, "awq_rmsnorm_fp8", tensors + [x8, sx], px, pr, pw, eps,
           None if h is None else h.data_ptr(), x8.data_ptr(), sx.data_ptr(), M, K)
     return (x8, sx) if h is None else (x8, sx, h)
@@ -364,7 +370,7 @@ def _gate_up(gate_up):
 def awq_silu_mul(gate_up, y=None):
     """gate_up fp16 [M][2F] -> y fp16 [M][F] = silu(gate_up[:, :F]) * gate_up[:, F:]."""
     M, F, p = _gate_up(gate_up)
-    y = _out(y, (M, F), torch.float16, "y", gate_up.device)
+    y = gate_up.new_empty((M, F)) if y is None else _given(y, (M, F), torch.float16, "y")
     _call(lib.awq_silu_mul, "awq_silu_mul", (gate_up, y), p, y.data_ptr(), M, F)
     return y
 
@@ -373,8 +379,8 @@ def awq_silu_mul_fp8(gate_up, x8=None, sx=None):
     """awq_silu_mul with y as (x8 uint8 E4M3 codes [M][F], sx float32 [M]), the
     inputs of awq_w4a8_gemm."""
     M, F, p = _gate_up(gate_up)
-    x8 = _out(x8, (M, F), torch.uint8, "x8", gate_up.device)
-    sx = _out(sx, (M,), torch.float32, "sx", gate_up.device)
+    x8 = gate_up.new_empty((M, F), dtype=torch.uint8) if x8 is None else _given(x8, (M, F), torch.uint8, "x8")
+    sx = gate_up.new_empty(M, dtype=torch.float32) if sx is None else _given(sx, (M,), torch.float32, "sx")
     _call(lib.awq_silu_mul_fp8, "awq_silu_mul_fp8", (gate_up, x8, sx), p, x8.data_ptr(), sx.data_ptr(), M, F)
     return x8, sx
 
@@ -464,7 +470,8 @@ def awq_kv8_attention(q, cache: Kv8Cache, starts, lens, block_table, workspace, 
     if head_dim != cache[0].shape[3]:
         raise ValueError(f"q must be [rows, q_heads, {cache[0].shape[3]}]")
     pq, sq = _kv8_rows(q, rows, q_heads, head_dim, "q")
-    y = _out(y, (rows, q_heads * head_dim), torch.float16, "y", q.device)
+    shape = (rows, q_heads * head_dim)
+    y = q.new_empty(shape) if y is None else _given(y, shape, torch.float16, "y")
     _kv8_call(lib.awq_kv8_attention, "awq_kv8_attention", rows, cache, starts, lens, block_table, workspace, (q, y),
               (pq, sq, q_heads, head_dim ** -0.5 if scale is None else scale), (y.data_ptr(),))
     return y

@@ -17,10 +17,11 @@
 
 #ifndef AT_S1
 #define AT_S1 2
-#define AT_S2 1
+#define AT_S2 2
 #define AT_C1 2
-#define AT_C2 3
+#define AT_C2 2
 #define AT_STAGES 3
+#define AT_COST 2
 #endif
 
 namespace awq {
@@ -265,6 +266,9 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
 // subnormals begin 2^-26 below the largest weight. p is rounded to fp16 (2^-11
 // relative) for the second MMA; l sums the unrounded p.
 constexpr float kPOffset = 12.f, kPMost = 15.f;
+// A group of units costs about as much again as this many units: its q, its
+// first copies' latency, the merge of the warps' parts.
+constexpr int kGroupCost = AT_COST;
 constexpr float kNoM = -1e30f;  // M of a row that has seen no key: far below any x, finite
 
 // The group of units that starts in a CTA's range and ends in a later one's.
@@ -319,9 +323,8 @@ struct Attn {
   static constexpr int kStages = AT_STAGES;
   static constexpr int kPartBytes = SUB * 16 * D;             // a warp's step of K, or of V
   static constexpr int kStageBytes = 2 * kPartBytes;
-  static constexpr int kMergeBytes = kWarps * kRows * (D + 4) * 4 + kWarps * kRows * 8;
-  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kSmem = (kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes) + 1024;  // room to align
+  static_assert(kStageBytes >= kRows * D * 4, "a warp's part of the output fits a stage");
+  static constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;  // room to align
   static constexpr int kSlot = kRows * (D + 2);
   static constexpr int kCtasPerSm = NT == 1 ? AT_C1 : AT_C2;          // 128 or 168 registers a thread
 };
@@ -340,6 +343,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
   __shared__ Place place;
   __shared__ __align__(8) uint64_t full[kWarps * L::kStages];
   __shared__ uint32_t abort_word;
+  __shared__ float2 ml[kWarps][L::kRows];  // M and l of the warps' rows
+  __shared__ const float* parts[kWarps];
   volatile uint32_t* const abort_flag = &abort_word;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWarps * L::kStages; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
   auto key_tiles = [&](const Seq& s) { return max((s.len + L::kKeys - 1) / L::kKeys, 1); };
   auto items = [&](int b) -> int64_t {
     const Seq s = load_seq(bt, b, status);
-    return row_tiles(s) * key_tiles(s) * cache.heads;
+    return row_tiles(s) * (key_tiles(s) + kGroupCost) * cache.heads;
   };
   int64_t before;
   const int64_t total = total_items(bt.seqs, items, scan, before);
@@ -379,43 +384,121 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
   int stage = 0, fill = 0;   // ring positions of the next step to use and to fill
   uint32_t parity = 0;
 
-  while (u < u1) {
-    Seq s = load_seq(bt, p.b, status);
-    int64_t n_seq = row_tiles(s) * key_tiles(s) * cache.heads;
-    while (u >= p.base + n_seq) {
-      p.base += n_seq;
-      s = load_seq(bt, ++p.b, status);
-      n_seq = row_tiles(s) * key_tiles(s) * cache.heads;
+  // ---- segments: the parts of groups in this CTA's range
+  struct Segment {
+    int b, row0, len, past, rows, r0, head, tile0, n;
+    bool starts, ends;
+    int64_t end;  // of the group, in units
+  } sg;
+  auto next_segment = [&]() -> bool {
+    while (u < u1) {
+      Seq s = load_seq(bt, p.b, status);
+      int64_t n_seq = row_tiles(s) * (key_tiles(s) + kGroupCost) * cache.heads;
+      while (u >= p.base + n_seq) {
+        p.base += n_seq;
+        s = load_seq(bt, ++p.b, status);
+        n_seq = row_tiles(s) * (key_tiles(s) + kGroupCost) * cache.heads;
+      }
+      const int per = key_tiles(s) + kGroupCost;
+      const int64_t in_seq = u - p.base, group_no = in_seq / per;
+      const int v0 = (int)(in_seq - group_no * per);
+      const int take = (int)(u1 - u < per - v0 ? u1 - u : per - v0);
+      sg.tile0 = max(v0 - kGroupCost, 0);
+      sg.n = v0 + take - kGroupCost - sg.tile0;
+      u += take;
+      if (sg.n <= 0) continue;  // only of the units that stand for the group's fixed cost
+      sg.head = (int)(group_no / row_tiles(s));
+      sg.r0 = (int)(group_no - (int64_t)sg.head * row_tiles(s)) * L::kRows;
+      sg.b = p.b;
+      sg.row0 = s.row0;
+      sg.len = s.len;
+      sg.past = s.len - s.tokens;
+      sg.rows = s.tokens * a.group;
+      sg.starts = sg.tile0 == 0;
+      sg.ends = v0 + take == per;
+      sg.end = p.base + (group_no + 1) * per;
+      return true;
     }
-    const int tiles = key_tiles(s);
-    const int64_t in_seq = u - p.base, group_no = in_seq / tiles;
-    const int tile0 = (int)(in_seq - group_no * tiles);
-    const int h = (int)(group_no / row_tiles(s));
-    const int row_tile = (int)(group_no - (int64_t)h * row_tiles(s));
-    const int n = (int)(u1 - u < tiles - tile0 ? u1 - u : tiles - tile0);
-    const int rows = s.tokens * a.group, r0 = row_tile * L::kRows;
-    const int past = s.len - s.tokens;
+    return false;
+  };
 
-    // ---- this segment's query rows as B fragments, channels in K's order
-    uint32_t qf[NT][KS][2];
+  // ---- a segment's query rows as B fragments, channels in K's order
+  uint32_t qf[NT][KS][2];
+  auto load_q = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + 8 * nt + g;
-      const __half* q = a.q + (int64_t)(s.row0 + r / a.group) * a.q_stride + ((int64_t)h * a.group + r % a.group) * D + 4 * t;
+      const int r = sg.r0 + 8 * nt + g;
+      const __half* q = a.q + (int64_t)(sg.row0 + r / a.group) * a.q_stride + ((int64_t)sg.head * a.group + r % a.group) * D + 4 * t;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint2 v = make_uint2(0, 0);
-        if (r < rows) v = *reinterpret_cast<const uint2*>(q + 16 * ks);
+        if (r < sg.rows) v = *reinterpret_cast<const uint2*>(q + 16 * ks);
         qf[nt][ks][0] = v.x;
         qf[nt][ks][1] = v.y;
       }
     }
+  };
+
+  // ---- the warp's steps of a segment
+  int key00, steps;  // first key, steps that have keys
+  auto begin_steps = [&]() {
+    key00 = sg.tile0 * L::kKeys + warp * 16 * SUB;
+    steps = sg.len > key00 ? min((sg.len - key00 + L::kKeys - 1) / L::kKeys, sg.n) : 0;
+  };
+  // Blocks and exponents of the next 32 subtiles, one per lane.
+  int blk = -1, exps = 0, exps_prev = 0;
+  auto load_info = [&](int sub0) {
+    const int sub = sub0 + lane, key = key00 + sub / SUB * L::kKeys + (sub % SUB) * 16;
+    exps_prev = exps;
+    blk = -1;
+    exps = 0;
+    if (sub < steps * SUB && key < sg.len) {
+      blk = bt.table[(int64_t)sg.b * bt.table_width + (key >> shift)];
+      if (blk < 0 || blk >= cache.blocks) {
+        record_status(status, AWQ_ERR_BOUNDS);
+        blk = -1;
+      } else {
+        const int64_t at = (int64_t)blk * cache.heads + sg.head;
+        exps = (uint8_t)cache.k_exp[at] | ((uint8_t)cache.v_exp[at] << 8);
+      }
+    }
+  };
+  // The boxes of a step: min(block, step) tokens each. A box of a block that
+  // is not there starts behind the cache's last row, which reads as zeros.
+  const int box = min(bs, 16 * SUB);
+  auto issue = [&](int step) {
+    if (step >= steps) return;
+    if ((step * SUB) % 32 == 0) load_info(step * SUB);
+    const uint32_t bar = bars + 8 * fill, dst = ring + fill * L::kStageBytes;
+    fill = fill == L::kStages - 1 ? 0 : fill + 1;
+    __syncwarp();  // every lane has read what the stage held
+    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
+    for (int i = 0; i < 16 * SUB; i += box) {
+      const int id = __shfl_sync(0xffffffffu, blk, step * SUB + i / 16);
+      const int row = id < 0 ? a.cache_rows : (id * cache.heads + sg.head) * bs + ((key00 + step * L::kKeys + i) & (bs - 1));
+      if (lane == 0) {
+        ptx::tma_load_2d(dst + i * D, &kmap, 0, row, bar);
+        ptx::tma_load_2d(dst + L::kPartBytes + i * D, &vmap, 0, row, bar);
+      }
+    }
+  };
+  auto begin_segment = [&]() {  // its first steps and its q on their way
+    begin_steps();
+#pragma unroll 1
+    for (int i = 0; i < L::kStages - 1; ++i) issue(i);
+    load_q();
+  };
+
+  bool dead = false;  // a wait gave up: no more copies, the results are garbage
+  bool have = next_segment();
+  if (have) begin_segment();
+  while (have) {
     int limit[NT][2];  // keys that the lane's two rows of each column tile see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) limit[nt][c] = min(past + (r0 + 8 * nt + 2 * t + c) / a.group + 1, s.len);
-    const int least = past + r0 / a.group + 1;  // keys that every row sees
+      for (int c = 0; c < 2; ++c) limit[nt][c] = min(sg.past + (sg.r0 + 8 * nt + 2 * t + c) / a.group + 1, sg.len);
+    const int least = sg.past + sg.r0 / a.group + 1;  // keys that every row sees
 
     float o[NT][MT][4], M[NT][2], l[NT][2];
 #pragma unroll
@@ -426,55 +509,9 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    // Blocks and exponents of the next 32 subtiles of this warp, one per lane.
-    const int* table = bt.table + (int64_t)p.b * bt.table_width;
-    const int key00 = tile0 * L::kKeys + warp * 16 * SUB;
-    auto key_of = [&](int sub) { return key00 + sub / SUB * L::kKeys + (sub % SUB) * 16; };
-    int blk = -1, exps = 0, exps_prev = 0;
-    auto load_info = [&](int sub0) {
-      const int sub = sub0 + lane, key = key_of(sub);
-      exps_prev = exps;
-      blk = -1;
-      exps = 0;
-      if (sub < n * SUB && key < s.len) {
-        blk = table[key >> shift];
-        if (blk < 0 || blk >= cache.blocks) {
-          record_status(status, AWQ_ERR_BOUNDS);
-          blk = -1;
-        } else {
-          const int64_t at = (int64_t)blk * cache.heads + h;
-          exps = (uint8_t)cache.k_exp[at] | ((uint8_t)cache.v_exp[at] << 8);
-        }
-      }
-    };
-    // Steps with keys of this warp, and the boxes that bring them: min(block,
-    // step) tokens each. A box of a block that is not there starts behind the
-    // cache's last row, which reads as zeros.
-    const int steps = s.len > key00 ? min((s.len - key00 + L::kKeys - 1) / L::kKeys, n) : 0;
-    const int box = min(bs, 16 * SUB);
-    auto issue = [&](int step) {
-      if (step >= steps) return;
-      if ((step * SUB) % 32 == 0) load_info(step * SUB);
-      const uint32_t bar = bars + 8 * fill, dst = ring + fill * L::kStageBytes;
-      fill = fill == L::kStages - 1 ? 0 : fill + 1;
-      __syncwarp();  // every lane has read what the stage held
-      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
-      for (int i = 0; i < 16 * SUB; i += box) {
-        const int id = __shfl_sync(0xffffffffu, blk, step * SUB + i / 16);
-        const int row = id < 0 ? a.cache_rows : (id * cache.heads + h) * bs + ((key00 + step * L::kKeys + i) & (bs - 1));
-        if (lane == 0) {
-          ptx::tma_load_2d(dst + i * D, &kmap, 0, row, bar);
-          ptx::tma_load_2d(dst + L::kPartBytes + i * D, &vmap, 0, row, bar);
-        }
-      }
-    };
-
-#pragma unroll 1
-    for (int i = 0; i < L::kStages - 1; ++i) issue(i);
-    for (int step = 0; step < steps; ++step) {
+    for (int step = 0; step < steps && !dead; ++step) {
       issue(step + L::kStages - 1);
-      ptx::wait_bar(bars + 8 * stage, parity, abort_flag, status);  // on a timeout the rest is garbage, soon over
-      __syncwarp();
+      dead = !__all_sync(0xffffffffu, ptx::wait_bar(bars + 8 * stage, parity, abort_flag, status));
       const uint32_t src = ring + stage * L::kStageBytes + lane_off;
       stage = stage == L::kStages - 1 ? 0 : stage + 1;
       parity ^= stage == 0;
@@ -616,67 +653,66 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
         }
       }
     }
-    if (*abort_flag)  // a wait gave up: no copy may land after this CTA is gone
-      for (int i = 0; i < L::kStages; ++i) ptx::drain_bar(bars + 8 * i, i < stage ? parity : parity ^ 1);
-
-    // ---- the four warps' parts of the segment
+    // ---- the next segment's copies start before this one's parts are merged
+    const Segment w = sg;
+    have = next_segment();
+    if (have && !dead) begin_segment();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int w = 4; w < 32; w <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], w);
-    float* mo = reinterpret_cast<float*>(smem);                    // [warp][row][D + 4]
-    float2* ml = reinterpret_cast<float2*>(mo + kWarps * L::kRows * (D + 4));  // [warp][row]
-    __syncthreads();  // every warp is done with the ring
+        for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+    // Each warp leaves its part in the stage of its ring that is still free.
+    // Columns are swapped by 16 in every second pair of rows: fewer conflicts.
+    float* const mine = reinterpret_cast<float*>(smem + (ring - ptx::smem_u32(smem)) + fill * L::kStageBytes);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int r = warp * L::kRows + 8 * nt + 2 * t + c;
+        const int r = 8 * nt + 2 * t + c;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-          *reinterpret_cast<float2*>(mo + r * (D + 4) + 16 * i + 2 * g) = make_float2(o[nt][i][c], o[nt][i][c + 2]);
-        if (g == 0) ml[r] = make_float2(M[nt][c], l[nt][c]);
+          *reinterpret_cast<float2*>(mine + r * D + ((16 * i + 2 * g) ^ ((t & 1) << 4))) = make_float2(o[nt][i][c], o[nt][i][c + 2]);
+        if (g == 0) ml[warp][r] = make_float2(M[nt][c], l[nt][c]);
       }
+    if (lane == 0) parts[warp] = mine;
     __syncthreads();
-    const bool starts_here = tile0 == 0, ends_here = tile0 + n == tiles;
-    float* slot = a.partial + ((int64_t)blockIdx.x * 2 + (starts_here ? 1 : 0)) * a.slot;
+    float* slot = a.partial + ((int64_t)blockIdx.x * 2 + (w.starts ? 1 : 0)) * a.slot;
     for (int i = tid; i < L::kRows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
-      if (r0 + r >= rows) continue;
+      if (w.r0 + r >= w.rows) continue;
       float mx = kNoM;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml[w * L::kRows + r].x);
+      for (int j = 0; j < kWarps; ++j) mx = fmaxf(mx, ml[j][r].x);
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       float den = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 v = ml[w * L::kRows + r];
+      for (int j = 0; j < kWarps; ++j) {
+        const float2 v = ml[j][r];
         const float f = ex2(v.x - mx);
-        const float4 ow = *reinterpret_cast<const float4*>(mo + (w * L::kRows + r) * (D + 4) + d);
+        const float4 ow = *reinterpret_cast<const float4*>(parts[j] + r * D + (d ^ ((r >> 1 & 1) << 4)));
         sum.x = fmaf(f, ow.x, sum.x), sum.y = fmaf(f, ow.y, sum.y);
         sum.z = fmaf(f, ow.z, sum.z), sum.w = fmaf(f, ow.w, sum.w);
         den = fmaf(f, v.y, den);
       }
-      if (starts_here && ends_here) {
+      if (w.starts && w.ends) {
         const float inv = den == 0.f ? 0.f : 1.f / den;  // a row that sees no key is zero
-        const int64_t at = (int64_t)(s.row0 + (r0 + r) / a.group) * cache.heads * a.group + (int64_t)h * a.group + (r0 + r) % a.group;
+        const int64_t at = (int64_t)(w.row0 + (w.r0 + r) / a.group) * cache.heads * a.group + (int64_t)w.head * a.group + (w.r0 + r) % a.group;
         *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(f2h(sum.x * inv, sum.y * inv), f2h(sum.z * inv, sum.w * inv));
       } else {
         *reinterpret_cast<float4*>(slot + r * D + d) = sum;
         if (d == 0) *reinterpret_cast<float2*>(slot + L::kRows * D + 2 * r) = make_float2(mx, den);
       }
     }
-    if (starts_here && !ends_here && tid == 0) {
-      // the CTA that holds the group's last unit: the last c with first_unit(c) < the group's end
-      const int64_t end = u + tiles;
-      a.fix[blockIdx.x] = Kv8Fix{1, s.row0, rows, r0, h, (int)((end * ctas + total - 1) / total) - 1, 0, 0};
-    }
-    u += n;
-    ptx::fence_proxy_async_smem();  // the merge buffer is the next segment's ring
-    if (__syncthreads_or(*abort_flag)) break;
+    if (w.starts && !w.ends && tid == 0)  // the CTA that holds the group's last unit: the last c with first_unit(c) < its end
+      a.fix[blockIdx.x] = Kv8Fix{1, w.row0, w.rows, w.r0, w.head, (int)((w.end * ctas + total - 1) / total) - 1, 0, 0};
+    ptx::fence_proxy_async_smem();  // copies will come where the parts were
+    if (__syncthreads_or(dead)) break;
   }
+  // After a timeout, copies still on their way must land before this CTA is gone.
+  for (; stage != fill; stage = stage == L::kStages - 1 ? 0 : stage + 1, parity ^= stage == 0)
+    ptx::drain_bar(bars + 8 * stage, parity);
 }
 
 // Adds the parts of the groups that more than one CTA worked on, in a fixed
