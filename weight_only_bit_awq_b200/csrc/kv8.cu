@@ -15,15 +15,6 @@
 #include "awq_internal.cuh"
 #include "sm100_ptx.cuh"
 
-#ifndef AT_S1
-#define AT_S1 2
-#define AT_S2 2
-#define AT_C1 2
-#define AT_C2 2
-#define AT_STAGES 3
-#define AT_COST 2
-#endif
-
 namespace awq {
 namespace {
 
@@ -268,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
 constexpr float kPOffset = 12.f, kPMost = 15.f;
 // A group of units costs about as much again as this many units: its q, its
 // first copies' latency, the merge of the warps' parts.
-constexpr int kGroupCost = AT_COST;
+constexpr int kGroupCost = 2;
 constexpr float kNoM = -1e30f;  // M of a row that has seen no key: far below any x, finite
 
 // The group of units that starts in a CTA's range and ends in a later one's.
@@ -320,13 +311,13 @@ template <int D, int SUB, int NT>
 struct Attn {
   static constexpr int kRows = 8 * NT;
   static constexpr int kKeys = kWarps * 16 * SUB;             // keys of a unit
-  static constexpr int kStages = AT_STAGES;
+  static constexpr int kStages = 3;
   static constexpr int kPartBytes = SUB * 16 * D;             // a warp's step of K, or of V
   static constexpr int kStageBytes = 2 * kPartBytes;
   static_assert(kStageBytes >= kRows * D * 4, "a warp's part of the output fits a stage");
   static constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;  // room to align
   static constexpr int kSlot = kRows * (D + 2);
-  static constexpr int kCtasPerSm = NT == 1 ? AT_C1 : AT_C2;          // 128 or 168 registers a thread
+  static constexpr int kCtasPerSm = 2;                        // by shared memory: 97 KB each
 };
 
 template <int D, int SUB, int NT>
@@ -798,7 +789,7 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem
 }
 
 constexpr int kMaxRows = 16;  // query rows of the widest tile
-constexpr int kMaxCtasPerSm = 4;
+constexpr int kMaxCtasPerSm = 2;
 
 template <int D, int SUB, int NT>
 cudaError_t launch_attention(AttnArgs a, const Kv8Cache& cache, const Kv8Batch& bt, uint32_t* status,
@@ -878,10 +869,10 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
   // rows that share a kv head, by the mean of new tokens a sequence (lengths are on the device)
   const int64_t rows = ((int64_t)bt.rows + bt.seqs - 1) / bt.seqs * a.group;
   if (cache.head_dim == 128)
-    return rows <= 8 ? launch_attention<128, AT_S1, 1>(a, cache, bt, status, stream)
-                     : launch_attention<128, AT_S2, 2>(a, cache, bt, status, stream);
-  return rows <= 8 ? launch_attention<64, 2*AT_S1, 1>(a, cache, bt, status, stream)
-                   : launch_attention<64, 2*AT_S2, 2>(a, cache, bt, status, stream);
+    return rows <= 8 ? launch_attention<128, 2, 1>(a, cache, bt, status, stream)
+                     : launch_attention<128, 2, 2>(a, cache, bt, status, stream);
+  return rows <= 8 ? launch_attention<64, 4, 1>(a, cache, bt, status, stream)
+                   : launch_attention<64, 4, 2>(a, cache, bt, status, stream);
 }
 
 }  // namespace awq
