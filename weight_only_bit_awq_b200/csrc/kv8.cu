@@ -128,10 +128,12 @@ __device__ __forceinline__ int needed_exponent(uint32_t mag) {
 // append
 // ---------------------------------------------------------------------------
 
-// One CTA per (block that gets new tokens, kv head, K or V). The block's new
-// rows stay in registers between the maximum and the conversion, so they are
-// read once. Bound by HBM for prompts (2 bytes read, 1 written an element),
-// by the launch for single tokens.
+// One CTA per (block that gets new tokens, kv head), for K and V. The block's
+// new rows stay in registers between the maximum and the conversion, so they
+// are read once, and their loads start before the block number is known.
+// Bound by HBM for prompts (2 bytes read, 1 written an element), by the launch
+// and four dependent loads for single tokens. Heads are the grid's fastest
+// dimension: the CTAs that run together read whole rows of k and v.
 template <int kIter>  // 16-byte pieces of a block's rows per thread: block_tokens * D / 1024
 __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __restrict__ knew,
                                                               const __half* __restrict__ vnew, int64_t k_stride,
@@ -139,89 +141,100 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
                                                               uint32_t* status) {
   __shared__ int64_t scan[kWarps];
   __shared__ Place place;
-  __shared__ uint32_t wmax[kWarps];
+  __shared__ uint32_t wmax[2][kWarps];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int bs = bt.block_tokens, D = cache.head_dim;
+  const int bs = bt.block_tokens, shift = __ffs(bs) - 1, D = cache.head_dim;
   // blocks of sequence b that get new tokens
   auto items = [&](int b) -> int64_t {
     const Seq s = load_seq(bt, b, status);
     const int first = max(s.len - s.tokens, 0);
-    return first < s.len && s.tokens > 0 ? (s.len - 1) / bs - first / bs + 1 : 0;
+    return first < s.len && s.tokens > 0 ? ((s.len - 1) >> shift) - (first >> shift) + 1 : 0;
   };
   int64_t before;
   const int64_t total = total_items(bt.seqs, items, scan, before);
-  const int64_t u = blockIdx.x;
+  const int64_t u = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
   if (u >= total) return;
   const Place p = find_item(bt.seqs, items, before, u, &place);
   const Seq s = load_seq(bt, p.b, status);
   const int past = s.len - s.tokens;  // position of the first new row (rows at negative positions have no place)
-  const int j = max(past, 0) / bs + (int)(u - p.base);
+  const int j = (max(past, 0) >> shift) + (int)(u - p.base);
+  const int h = blockIdx.x;
+  const int lo = max(max(past, 0) - j * bs, 0), hi = min(s.len - j * bs, bs);  // new rows of the block
+  const int pieces = D / 8, rows_per_pass = kThreads / pieces;
+  const int r0 = threadIdx.x / pieces, c = threadIdx.x % pieces;
+  const int64_t row0 = (int64_t)s.row0 + (int64_t)j * bs - past;  // source row of the block's token 0
+
+  uint4 x[2][kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int r = r0 + i * rows_per_pass;
+    const int64_t at = (int64_t)h * D + 8 * c;
+    x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
+    if (r >= lo && r < hi) {
+      x[0][i] = *reinterpret_cast<const uint4*>(knew + (row0 + r) * k_stride + at);
+      x[1][i] = *reinterpret_cast<const uint4*>(vnew + (row0 + r) * v_stride + at);
+    }
+  }
   const int blk = bt.table[(int64_t)p.b * bt.table_width + j];
   if (blk < 0 || blk >= cache.blocks) {
     if (threadIdx.x == 0) record_status(status, AWQ_ERR_BOUNDS);
     return;
   }
-  const int h = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
-  const int lo = max(max(past, 0) - j * bs, 0), hi = min(s.len - j * bs, bs);  // new rows of the block
-  const int pieces = D / 8, rows_per_pass = kThreads / pieces;
-  const int r0 = threadIdx.x / pieces, c = threadIdx.x % pieces;
-  const __half* src = (is_v ? vnew : knew) + (int64_t)h * D + 8 * c;
-  const int64_t stride = is_v ? v_stride : k_stride;
-  const int64_t row0 = (int64_t)s.row0 + (int64_t)j * bs - past;  // source row of the block's token 0
-
-  uint4 x[kIter];
-  uint32_t mag = 0;
+  const int64_t at = (int64_t)blk * cache.heads + h;
+  int8_t* const exps[2] = {cache.k_exp + at, cache.v_exp + at};
+  int e_old[2];
 #pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    const int r = r0 + i * rows_per_pass;
-    x[i] = r >= lo && r < hi ? *reinterpret_cast<const uint4*>(src + (row0 + r) * stride) : make_uint4(0, 0, 0, 0);
-  }
+  for (int part = 0; part < 2; ++part) {
+    e_old[part] = lo > 0 ? (int)*exps[part] : -128;
+    uint32_t mag = 0;
 #pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    for (int i = 0; i < kIter; ++i) {
+      const uint32_t w[4] = {x[part][i].x, x[part][i].y, x[part][i].z, x[part][i].w};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t a = w[q] & 0x7FFFu, b = (w[q] >> 16) & 0x7FFFu;
-      if (a < 0x7C00u) mag = max(mag, a);  // infinities and NaN become NaN codes and set no scale
-      if (b < 0x7C00u) mag = max(mag, b);
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t a = w[q] & 0x7FFFu, b = (w[q] >> 16) & 0x7FFFu;
+        if (a < 0x7C00u) mag = max(mag, a);  // infinities and NaN become NaN codes and set no scale
+        if (b < 0x7C00u) mag = max(mag, b);
+      }
     }
+    mag = __reduce_max_sync(0xffffffffu, mag);
+    if ((threadIdx.x & 31) == 0) wmax[part][threadIdx.x >> 5] = mag;
   }
-  mag = __reduce_max_sync(0xffffffffu, mag);
-  if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = mag;
-  int8_t* exps = (is_v ? cache.v_exp : cache.k_exp) + (int64_t)blk * cache.heads + h;
-  const int e_old = lo > 0 ? (int)*exps : -128;
-  __syncthreads();
+  __syncthreads();  // the maxima are there, and every thread has read the old exponents
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) mag = max(mag, wmax[w]);
-  const int e = max(needed_exponent(mag), e_old);
-  if (threadIdx.x == 0) *exps = (int8_t)e;
-  uint8_t* dst = (is_v ? cache.v : cache.k) + ((int64_t)blk * cache.heads + h) * bs * D + 8 * c;
-  const float inv = ldexpf(1.f, -e);
+  for (int part = 0; part < 2; ++part) {
+    uint32_t mag = 0;
 #pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    const int r = r0 + i * rows_per_pass;
-    if (r < lo || r >= hi) continue;
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint32_t o[4];
+    for (int w = 0; w < kWarps; ++w) mag = max(mag, wmax[part][w]);
+    const int e = max(needed_exponent(mag), e_old[part]);
+    if (threadIdx.x == 0) *exps[part] = (int8_t)e;
+    uint8_t* dst = (part ? cache.v : cache.k) + at * bs * D + 8 * c;
+    const float inv = ldexpf(1.f, -e);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float2 f = h2f(w[q]);
-      f.x = fabsf(f.x) <= 65504.f ? f.x * inv : NAN;  // exact; the conversion would saturate an infinity
-      f.y = fabsf(f.y) <= 65504.f ? f.y * inv : NAN;
-      o[q] = code2(f.x, f.y);
+    for (int i = 0; i < kIter; ++i) {
+      const int r = r0 + i * rows_per_pass;
+      if (r < lo || r >= hi) continue;
+      const uint32_t w[4] = {x[part][i].x, x[part][i].y, x[part][i].z, x[part][i].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float2 f = h2f(w[q]);
+        f.x = fabsf(f.x) <= 65504.f ? f.x * inv : NAN;  // exact; the conversion would saturate an infinity
+        f.y = fabsf(f.y) <= 65504.f ? f.y * inv : NAN;
+        o[q] = code2(f.x, f.y);
+      }
+      *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
     }
-    *reinterpret_cast<uint2*>(dst + (int64_t)r * D) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
-  }
-  if (e > e_old && lo > 0) {  // the codes that were there, under the larger exponent
-    const float down = ldexpf(1.f, e_old - e);
-    for (int r = r0; r < lo; r += rows_per_pass) {
-      uint2* at = reinterpret_cast<uint2*>(dst + (int64_t)r * D);
-      const uint2 v = *at;
-      const float2 a = h2f(lo_h2(v.x)), b = h2f(hi_h2(v.x)), d = h2f(lo_h2(v.y)), f = h2f(hi_h2(v.y));
-      *at = make_uint2(code2(a.x * down, a.y * down) | (code2(b.x * down, b.y * down) << 16),
-                       code2(d.x * down, d.y * down) | (code2(f.x * down, f.y * down) << 16));
+    if (e > e_old[part] && lo > 0) {  // the codes that were there, under the larger exponent
+      const float down = ldexpf(1.f, e_old[part] - e);
+      for (int r = r0; r < lo; r += rows_per_pass) {
+        uint2* old = reinterpret_cast<uint2*>(dst + r * D);
+        const uint2 v = *old;
+        const float2 a = h2f(lo_h2(v.x)), b = h2f(hi_h2(v.x)), d = h2f(lo_h2(v.y)), f = h2f(hi_h2(v.y));
+        *old = make_uint2(code2(a.x * down, a.y * down) | (code2(b.x * down, b.y * down) << 16),
+                          code2(d.x * down, d.y * down) | (code2(f.x * down, f.y * down) << 16));
+      }
     }
   }
 }
@@ -841,7 +854,8 @@ cudaError_t launch_kv8_append(const __half* k, const __half* v, int64_t k_stride
   // per full block of them and two at the ends
   int64_t items = (int64_t)bt.rows / bt.block_tokens + 2 * (int64_t)bt.seqs;
   if (items > bt.rows) items = bt.rows;
-  const dim3 grid((unsigned)items, 2 * cache.heads);
+  const unsigned gy = items < 65535 ? (unsigned)items : 65535u;
+  const dim3 grid(cache.heads, gy, (unsigned)((items + gy - 1) / gy));
   switch (bt.block_tokens * cache.head_dim / 1024) {
     case 1: return launch_pdl(kv8_append_kernel<1>, grid, kThreads, 0, stream, k, v, k_stride, v_stride, cache, bt, status);
     case 2: return launch_pdl(kv8_append_kernel<2>, grid, kThreads, 0, stream, k, v, k_stride, v_stride, cache, bt, status);

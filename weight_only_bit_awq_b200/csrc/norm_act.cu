@@ -53,26 +53,36 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// Sum of `s` and maximum of `m` over the CTA; `red` holds two buffers that
-// alternate from row to row, so one barrier a row is enough.
-__device__ __forceinline__ void block_sum_max(float& s, float& m, float2* red, int parity) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  }
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Largest |v| as the bits of fp32: a NaN is above infinity, infinity above
+// every number, so the maximum also tells a row that is not finite.
+__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Sum of `s` (kSum) and maximum of `m` (kMax) over the CTA; `red` holds two
+// buffers that alternate from row to row, so one barrier a row is enough.
+template <bool kSum, bool kMax>
+__device__ __forceinline__ void block_reduce(float& s, uint32_t& m, uint2* red, int parity) {
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  red += 32 * parity;
-  if (lane == 0) red[threadIdx.x >> 5] = make_float2(s, m);
-  __syncthreads();
-  const float2 v = lane < warps ? red[lane] : make_float2(0.f, 0.f);
-  s = v.x;
-  m = v.y;
+  auto warp_reduce = [&]() {
+    if (kMax) m = __reduce_max_sync(0xffffffffu, m);
+    if (kSum) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  }
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    }
+  };
+  warp_reduce();
+  red += 32 * parity;
+  if (lane == 0) red[threadIdx.x >> 5] = make_uint2(__float_as_uint(s), m);
+  __syncthreads();
+  const uint2 v = lane < warps ? red[lane] : make_uint2(0, 0);
+  s = __uint_as_float(v.x);
+  m = v.y;
+  warp_reduce();
 }
 
 struct NormArgs {
@@ -80,17 +90,17 @@ struct NormArgs {
   __half *h, *y;
   uint8_t* x8;
   float* sx;
-  float eps;
+  float eps, inv_k;  // inv_k: 1 / K
   int64_t M;
   int K8;  // 8-element vectors of a row
 };
 
 // The row factor of y (fp16 output) or of the codes (E4M3 output, where the
-// row's scale is stored too). A row with an infinity or a NaN has a sum that
-// is not finite: its y, or its sx, is not finite either.
+// row's scale is stored too); m: largest |h w|. A row with an infinity or a NaN
+// has a sum that is not finite: its y, or its sx, is not finite either.
 template <bool kFp8>
-__device__ __forceinline__ float norm_factor(const NormArgs& a, int64_t row, float sum, float mx) {
-  const float rs = rsqrtf(sum / (float)((int64_t)a.K8 * 8) + a.eps);
+__device__ __forceinline__ float norm_factor(const NormArgs& a, int64_t row, float sum, uint32_t m) {
+  const float rs = rsqrtf(sum * a.inv_k + a.eps), mx = __uint_as_float(m);
   if (!kFp8) return rs;
   if (threadIdx.x == 0) a.sx[row] = sum - sum == 0.f ? mx * rs * (1.f / kE4m3Max) : sum - sum;
   return mx > 0.f ? kE4m3Max / mx : 0.f;
@@ -99,7 +109,7 @@ __device__ __forceinline__ float norm_factor(const NormArgs& a, int64_t row, flo
 // One CTA a row at a time, the row in V vectors of 8 per thread.
 template <int V, bool kRes, bool kFp8>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
-  __shared__ float2 red[64];
+  __shared__ uint2 red[64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int NT = blockDim.x, tid = threadIdx.x;
@@ -119,7 +129,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
       vx[i] = c < a.K8 ? reinterpret_cast<const uint4*>(a.x)[base + c] : make_uint4(0, 0, 0, 0);
       if (kRes) vr[i] = c < a.K8 ? reinterpret_cast<const uint4*>(a.residual)[base + c] : make_uint4(0, 0, 0, 0);
     }
-    float h[V][8], sum = 0.f, mx = 0.f;
+    float h[V][8], sum = 0.f;
+    uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       unpack8(vx[i], h[i]);
@@ -137,10 +148,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
       for (int j = 0; j < 8; ++j) {
         sum = fmaf(h[i][j], h[i][j], sum);
         h[i][j] *= wf[j];
-        if (kFp8) mx = fmaxf(mx, fabsf(h[i][j]));
+        if (kFp8) mx = max(mx, mag(h[i][j]));
       }
     }
-    block_sum_max(sum, mx, red, parity);
+    block_reduce<true, kFp8>(sum, mx, red, parity);
     const float f = norm_factor<kFp8>(a, row, sum, mx);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -162,13 +173,14 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
 // still be x or the residual.
 template <bool kRes, bool kFp8>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
-  __shared__ float2 red[64];
+  __shared__ uint2 red[64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
     const int64_t base = row * a.K8;
-    float h[8], r[8], wf[8], sum = 0.f, mx = 0.f;
+    float h[8], r[8], wf[8], sum = 0.f;
+    uint32_t mx = 0;
     for (int c = threadIdx.x; c < a.K8; c += blockDim.x) {
       unpack8(reinterpret_cast<const uint4*>(a.x)[base + c], h);
       if (kRes) unpack8(reinterpret_cast<const uint4*>(a.residual)[base + c], r);
@@ -177,10 +189,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
       for (int j = 0; j < 8; ++j) {
         if (kRes) h[j] += r[j];
         sum = fmaf(h[j], h[j], sum);
-        mx = fmaxf(mx, fabsf(h[j] * wf[j]));
+        if (kFp8) mx = max(mx, mag(h[j] * wf[j]));
       }
     }
-    block_sum_max(sum, mx, red, parity);
+    block_reduce<true, kFp8>(sum, mx, red, parity);
     const float f = norm_factor<kFp8>(a, row, sum, mx);
     for (int c = threadIdx.x; c < a.K8; c += blockDim.x) {
       unpack8(reinterpret_cast<const uint4*>(a.x)[base + c], h);
@@ -219,7 +231,7 @@ __device__ __forceinline__ void silu8(const uint4& vg, const uint4& vu, float (&
   unpack8(vg, y);
   unpack8(vu, u);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = __fdividef(y[j], 1.f + ex2(-kLog2e * y[j])) * u[j];
+  for (int j = 0; j < 8; ++j) y[j] = y[j] * rcp(1.f + ex2(-kLog2e * y[j])) * u[j];  // 1 / inf is 0
 }
 
 // fp16 output: no reduction, a CTA takes blockDim * V vectors of one row.
@@ -245,27 +257,27 @@ __global__ void __launch_bounds__(256) silu_mul_kernel(const SiluArgs a) {
   }
 }
 
-// Stores sx of a row whose largest |y| is mx and whose sum of y - y is `bad`
-// (0, or NaN when the row holds something that is not finite), and returns
-// the codes' factor 1 / sx. Below 2^-100 that factor would overflow fp32:
+// Stores sx of a row whose largest |y| is m (bits), and returns the codes'
+// factor 1 / sx. Below 2^-100 that factor would overflow fp32:
 // such a row counts as zero (a y below 2^-25 is zero in fp16 too).
-__device__ __forceinline__ float silu_factor(const SiluArgs& a, int64_t row, float bad, float mx) {
-  if (mx < 0x1p-100f) mx = 0.f;
-  if (threadIdx.x == 0) a.sx[row] = bad == 0.f ? mx * (1.f / kE4m3Max) : bad;
+__device__ __forceinline__ float silu_factor(const SiluArgs& a, int64_t row, uint32_t m) {
+  const float mx = m < __float_as_uint(0x1p-100f) ? 0.f : __uint_as_float(m);
+  if (threadIdx.x == 0) a.sx[row] = mx * (1.f / kE4m3Max);  // infinity and NaN stay
   return mx > 0.f ? kE4m3Max / mx : 0.f;
 }
 
 // E4M3 output: one CTA a row at a time, the row in registers.
 template <int V>
 __global__ void __launch_bounds__(1024) silu_mul_fp8_kernel(const SiluArgs a) {
-  __shared__ float2 red[64];
+  __shared__ uint2 red[64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int NT = blockDim.x, tid = threadIdx.x;
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
     const uint4* g = reinterpret_cast<const uint4*>(a.gu) + row * 2 * a.F8;
-    float y[V][8], bad = 0.f, mx = 0.f;
+    float y[V][8], none = 0.f;
+    uint32_t mx = 0;
     uint4 vg[V], vu[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -277,13 +289,10 @@ __global__ void __launch_bounds__(1024) silu_mul_fp8_kernel(const SiluArgs a) {
     for (int i = 0; i < V; ++i) {
       silu8(vg[i], vu[i], y[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mx = fmaxf(mx, fabsf(y[i][j]));
-        bad += y[i][j] - y[i][j];
-      }
+      for (int j = 0; j < 8; ++j) mx = max(mx, mag(y[i][j]));
     }
-    block_sum_max(bad, mx, red, parity);
-    const float f = silu_factor(a, row, bad, mx);
+    block_reduce<false, true>(none, mx, red, parity);
+    const float f = silu_factor(a, row, mx);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * NT + tid;
@@ -294,23 +303,21 @@ __global__ void __launch_bounds__(1024) silu_mul_fp8_kernel(const SiluArgs a) {
 
 // E4M3 output of rows too long for the registers of one CTA: read twice.
 __global__ void __launch_bounds__(1024) silu_mul_fp8_long_kernel(const SiluArgs a) {
-  __shared__ float2 red[64];
+  __shared__ uint2 red[64];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
     const uint4* g = reinterpret_cast<const uint4*>(a.gu) + row * 2 * a.F8;
-    float y[8], bad = 0.f, mx = 0.f;
+    float y[8], none = 0.f;
+    uint32_t mx = 0;
     for (int c = threadIdx.x; c < a.F8; c += blockDim.x) {
       silu8(g[c], g[a.F8 + c], y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mx = fmaxf(mx, fabsf(y[j]));
-        bad += y[j] - y[j];
-      }
+      for (int j = 0; j < 8; ++j) mx = max(mx, mag(y[j]));
     }
-    block_sum_max(bad, mx, red, parity);
-    const float f = silu_factor(a, row, bad, mx);
+    block_reduce<false, true>(none, mx, red, parity);
+    const float f = silu_factor(a, row, mx);
     for (int c = threadIdx.x; c < a.F8; c += blockDim.x) {
       silu8(g[c], g[a.F8 + c], y);
       reinterpret_cast<uint2*>(a.x8)[row * a.F8 + c] = codes8(y, f);
@@ -355,7 +362,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_rmsnorm(const __half* x, const __half* residual, const __half* w, float eps, __half* h, __half* y,
                            uint8_t* x8, float* sx, int64_t M, int64_t K, cudaStream_t stream) {
-  const NormArgs a{x, residual, w, h, y, x8, sx, eps, M, (int)(K / 8)};
+  const NormArgs a{x, residual, w, h, y, x8, sx, eps, 1.f / (float)K, M, (int)(K / 8)};
   if (residual) return x8 ? launch_norm<true, true>(a, stream) : launch_norm<true, false>(a, stream);
   return x8 ? launch_norm<false, true>(a, stream) : launch_norm<false, false>(a, stream);
 }
