@@ -423,18 +423,19 @@ def _kv8_rows(t, rows, heads, head_dim, name):
     apart (a column range of a wider matrix)."""
     if not t.is_cuda or t.dtype != torch.float16:
         raise ValueError(f"{name} must be a CUDA tensor of torch.float16")
-    if tuple(t.shape) != (rows, heads, head_dim):
+    if t.shape != (rows, heads, head_dim):
         raise ValueError(f"{name} must be [{rows}, {heads}, {head_dim}]")
-    stride = t.stride()
-    if stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
+    stride, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != head_dim):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), (stride[0] if rows > 1 else heads * head_dim)
+    return t.data_ptr(), (stride if rows > 1 else heads * head_dim)
 
 
 def _kv8_call(fn, name, rows, cache, starts, lens, table, workspace, tensors, before, after):
     k, v, k_exp, v_exp = cache
-    blocks, heads, block_tokens, head_dim = k.shape
-    if v.shape != k.shape or k_exp.shape != k.shape[:2] or v_exp.shape != k.shape[:2]:
+    shape = k.shape
+    blocks, heads, block_tokens, head_dim = shape
+    if v.shape != shape or k_exp.shape != (blocks, heads) or v_exp.shape != (blocks, heads):
         raise ValueError("cache parts must be [blocks, heads, block_tokens, head_dim] and [blocks, heads]")
     c = _Kv8Cache(_dev(k, torch.uint8, "cache.k"), _dev(v, torch.uint8, "cache.v"),
                   _dev(k_exp, torch.int8, "cache.k_exp"), _dev(v_exp, torch.int8, "cache.v_exp"), blocks, heads,
@@ -444,8 +445,8 @@ def _kv8_call(fn, name, rows, cache, starts, lens, table, workspace, tensors, be
         raise ValueError(f"starts must be [{seqs + 1}] and lens [{seqs}]")
     b = _Kv8Batch(_dev(starts, torch.int32, "starts"), _dev(lens, torch.int32, "lens"),
                   _dev(table, torch.int32, "block_table"), rows, seqs, width)
-    _call(fn, name, (k, v, k_exp, v_exp, starts, lens, table, workspace, *tensors), *before, ctypes.byref(c),
-          ctypes.byref(b), *after, _dev(workspace, torch.uint8, "workspace"), workspace.numel())
+    _call(fn, name, (k, v, k_exp, v_exp, starts, lens, table, workspace, *tensors), *before, c, b, *after,
+          _dev(workspace, torch.uint8, "workspace"), workspace.numel())
 
 
 def awq_kv8_append(k, v, cache: Kv8Cache, starts, lens, block_table, workspace):

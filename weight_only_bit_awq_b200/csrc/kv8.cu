@@ -115,6 +115,22 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// Largest magnitudes of the low and the high fp16 values, as bits; of all
+// finite ones.
+__device__ __forceinline__ uint32_t max_mag(const uint4& v) {
+  constexpr uint32_t k = 0x7FFF7FFFu;
+  return __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+}
+__device__ __forceinline__ uint32_t max_finite_mag(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+  for (int q = 0; q < 8; ++q) {
+    const uint32_t a = w[q / 2] >> 16 * (q & 1) & 0x7FFFu;
+    if (a < 0x7C00u) m = max(m, a);
+  }
+  return m;
+}
+
 // Smallest e with |v| <= 448 2^e for the fp16 magnitude bits of a finite v:
 // v = 1.m 2^x in fp32, 448 = 1.75 * 2^8. Zero needs the least, -32 (what
 // 2^-24, the smallest fp16, needs).
@@ -184,19 +200,18 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
   const int64_t at = (int64_t)blk * cache.heads + h;
   int8_t* const exps[2] = {cache.k_exp + at, cache.v_exp + at};
   int e_old[2];
+  bool odd[2];  // this thread has an infinity or a NaN
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
     e_old[part] = lo > 0 ? (int)*exps[part] : -128;
-    uint32_t mag = 0;
+    uint32_t m2 = 0;  // two maxima of fp16 magnitudes
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-      const uint32_t w[4] = {x[part][i].x, x[part][i].y, x[part][i].z, x[part][i].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t a = w[q] & 0x7FFFu, b = (w[q] >> 16) & 0x7FFFu;
-        if (a < 0x7C00u) mag = max(mag, a);  // infinities and NaN become NaN codes and set no scale
-        if (b < 0x7C00u) mag = max(mag, b);
-      }
+    for (int i = 0; i < kIter; ++i) m2 = __vmaxu2(m2, max_mag(x[part][i]));
+    uint32_t mag = max(m2 & 0xFFFFu, m2 >> 16);
+    odd[part] = mag >= 0x7C00u;
+    if (odd[part]) {  // infinities and NaN become NaN codes and set no scale: once more, without them
+      mag = 0;
+      for (int i = 0; i < kIter; ++i) mag = max(mag, max_finite_mag(x[part][i]));
     }
     mag = __reduce_max_sync(0xffffffffu, mag);
     if ((threadIdx.x & 31) == 0) wmax[part][threadIdx.x >> 5] = mag;
@@ -220,8 +235,11 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float2 f = h2f(w[q]);
-        f.x = fabsf(f.x) <= 65504.f ? f.x * inv : NAN;  // exact; the conversion would saturate an infinity
-        f.y = fabsf(f.y) <= 65504.f ? f.y * inv : NAN;
+        f.x *= inv, f.y *= inv;  // exact
+        if (odd[part]) {  // the conversion would saturate an infinity
+          if (!(fabsf(f.x) < INFINITY)) f.x = NAN;
+          if (!(fabsf(f.y) < INFINITY)) f.y = NAN;
+        }
         o[q] = code2(f.x, f.y);
       }
       *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
