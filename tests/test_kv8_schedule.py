@@ -1,5 +1,5 @@
 """Host model of the cache attention's work split (csrc/kv8.cu): units of
-128 keys (256 for 64-wide heads) of one group (sequence, kv head, row tile),
+128 keys of one group (sequence, kv head, row tile),
 behind two units per group that stand for its fixed cost and hold no keys;
 equal contiguous ranges of them per CTA; and the hand-over of groups that
 several CTAs work on to the fixup kernel. Checked on random ragged batches: every unit
@@ -80,8 +80,8 @@ def test_every_unit_once_and_every_group_written_once(seed):
         B = rng.randint(1, 20)
         seqs = [(rng.choice([0, 1, 1, 1, rng.randint(2, 40)]), rng.choice([0, 1, rng.randint(1, 300), rng.randint(1, 9000)]))
                 for _ in range(B)]
-        simulate(seqs, rng.choice([1, 4, 8, 29]), rng.choice([1, 2, 8]), rng.choice([8, 16]), rng.choice([128, 256]),
-                 rng.choice([1, 3, 148, 296]))
+        simulate(seqs, rng.choice([1, 4, 8, 29]), rng.choice([1, 2, 8]), rng.choice([8, 16]), 128,
+                 rng.choice([1, 3, 148, 296, 444]))
 
 
 def test_long_and_empty_batches():

@@ -336,27 +336,27 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t a, uint32_t (&r)[4]) {
 }
 
 // D: head dimension; SUB: 16-key subtiles of a warp's step; NT: column tiles
-// of 8 query rows. A unit of work is 4 warps x 16 SUB keys of one (sequence,
+// of 8 query rows; ST: steps in a warp's ring. A unit of work is 4 warps x 16 SUB keys of one (sequence,
 // kv head, row tile).
-template <int D, int SUB, int NT>
+template <int D, int SUB, int NT, int ST>
 struct Attn {
   static constexpr int kRows = 8 * NT;
   static constexpr int kKeys = kWarps * 16 * SUB;             // keys of a unit
-  static constexpr int kStages = 3;
+  static constexpr int kStages = ST;
   static constexpr int kPartBytes = SUB * 16 * D;             // a warp's step of K, or of V
   static constexpr int kStageBytes = 2 * kPartBytes;
   static_assert(kStageBytes >= kRows * D * 4, "a warp's part of the output fits a stage");
   static constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;  // room to align
   static constexpr int kSlot = kRows * (D + 2);
-  static constexpr int kCtasPerSm = 2;                        // by shared memory: 97 KB each
+  static constexpr int kCtasPerSm = kStages * kStageBytes <= 16384 ? 3 : 2;  // by shared memory and registers
 };
 
-template <int D, int SUB, int NT>
-__global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
+template <int D, int SUB, int NT, int ST>
+__global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
     kv8_attention_kernel(const AttnArgs a, const Kv8Cache cache, const Kv8Batch bt,
                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          uint32_t* status) {
-  using L = Attn<D, SUB, NT>;
+  using L = Attn<D, SUB, NT, ST>;
   constexpr int KS = D / 16;     // k-steps of S
   constexpr int MT = D / 16;     // channel tiles of O
   extern __shared__ char smem_raw[];
@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
   // ---- segments: the parts of groups in this CTA's range
   struct Segment {
     int b, row0, len, past, rows, r0, head, tile0, n;
+    int seen;     // keys that some row sees
     bool starts, ends;
     int64_t end;  // of the group, in units
   } sg;
@@ -436,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
       sg.len = s.len;
       sg.past = s.len - s.tokens;
       sg.rows = s.tokens * a.group;
+      sg.seen = max(min(sg.past + (min(sg.r0 + L::kRows, sg.rows) - 1) / a.group + 1, s.len), 0);
       sg.starts = sg.tile0 == 0;
       sg.ends = v0 + take == per;
       sg.end = p.base + (group_no + 1) * per;
@@ -462,26 +464,29 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
   };
 
   // ---- the warp's steps of a segment
-  int key00, steps;  // first key, steps that have keys
+  int key00, steps;  // first key, steps with keys that some row sees
   auto begin_steps = [&]() {
     key00 = sg.tile0 * L::kKeys + warp * 16 * SUB;
-    steps = sg.len > key00 ? min((sg.len - key00 + L::kKeys - 1) / L::kKeys, sg.n) : 0;
+    steps = sg.seen > key00 ? min((sg.seen - key00 + L::kKeys - 1) / L::kKeys, sg.n) : 0;
   };
   // Blocks and exponents of the next 32 subtiles, one per lane.
-  int blk = -1, exps = 0, exps_prev = 0;
+  int blk = -1;
+  float k_exp = 0.f, v_exp = 0.f, k_exp_prev = 0.f, v_exp_prev = 0.f;  // scale log2(e) 2^e_k; e_v
   auto load_info = [&](int sub0) {
     const int sub = sub0 + lane, key = key00 + sub / SUB * L::kKeys + (sub % SUB) * 16;
-    exps_prev = exps;
+    k_exp_prev = k_exp;
+    v_exp_prev = v_exp;
     blk = -1;
-    exps = 0;
-    if (sub < steps * SUB && key < sg.len) {
+    k_exp = v_exp = 0.f;
+    if (sub < steps * SUB && key < sg.seen) {
       blk = bt.table[(int64_t)sg.b * bt.table_width + (key >> shift)];
       if (blk < 0 || blk >= cache.blocks) {
         record_status(status, AWQ_ERR_BOUNDS);
         blk = -1;
       } else {
         const int64_t at = (int64_t)blk * cache.heads + sg.head;
-        exps = (uint8_t)cache.k_exp[at] | ((uint8_t)cache.v_exp[at] << 8);
+        k_exp = a.scale_log2 * __int_as_float(((int)cache.k_exp[at] + 127) << 23);
+        v_exp = (float)cache.v_exp[at];
       }
     }
   };
@@ -527,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      M[nt][0] = M[nt][1] = kNoM;
+      M[nt][0] = M[nt][1] = steps > 0 ? 0.f : kNoM;  // 0 until the first step sets it
       l[nt][0] = l[nt][1] = 0.f;
     }
 
@@ -539,9 +544,10 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
       parity ^= stage == 0;
       const int key0 = key00 + step * L::kKeys;
       // the issuing side is up to kStages - 1 steps ahead: it may have loaded the next 32 already
-      const int e_of = (step * SUB) / 32 == min(step + L::kStages - 1, steps - 1) * SUB / 32 ? exps : exps_prev;
+      const bool same = (step * SUB) / 32 == min(step + L::kStages - 1, steps - 1) * SUB / 32;
+      const float k_of = same ? k_exp : k_exp_prev, v_of = same ? v_exp : v_exp_prev;
 
-      // x + e_v of the step's keys (masked keys: -inf)
+      // The weights' exponents x + e_v - M of the step's keys (masked keys: -inf)
       float x[SUB][NT][4], unit[SUB];  // unit: 2^-e_v
 #pragma unroll
       for (int sb = 0; sb < SUB; ++sb)
@@ -562,14 +568,13 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
         }
 #pragma unroll
       for (int sb = 0; sb < SUB; ++sb) {
-        const int e2 = __shfl_sync(0xffffffffu, e_of, step * SUB + sb);
-        const float k_unit = a.scale_log2 * __int_as_float(((int)(int8_t)e2 + 127) << 23);
-        const int ev = (int)(e2 << 16) >> 24;
-        unit[sb] = __int_as_float((127 - ev) << 23);
+        const float k_unit = __shfl_sync(0xffffffffu, k_of, step * SUB + sb);
+        const float ev = __shfl_sync(0xffffffffu, v_of, step * SUB + sb);
+        unit[sb] = ex2(-ev);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[sb][nt][c] = fmaf(x[sb][nt][c], k_unit, (float)ev);
+          for (int c = 0; c < 4; ++c) x[sb][nt][c] = fmaf(x[sb][nt][c], k_unit, ev - M[nt][c & 1]);
       }
       if (key0 + 16 * SUB > least) {  // some row does not see all of the step's keys
 #pragma unroll
@@ -581,31 +586,36 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
               if (key0 + 16 * sb + g + 8 * (c >> 1) >= limit[nt][c & 1]) x[sb][nt][c] = -INFINITY;
       }
 
-      // Where a weight's exponent x - M exceeds kPMost (or a row has no M yet),
-      // every row's M follows its running maximum.
+      // Where one exceeds kPMost, and in a segment's first step, every row's M
+      // follows its running maximum.
       float over = -INFINITY;
 #pragma unroll
       for (int sb = 0; sb < SUB; ++sb)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) over = fmaxf(over, x[sb][nt][c] - M[nt][c & 1]);
-      if (__any_sync(0xffffffffu, over > kPMost)) {
+          for (int c = 0; c < 4; ++c) over = fmaxf(over, x[sb][nt][c]);
+      if (__any_sync(0xffffffffu, over > kPMost) || step == 0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float f[2];
+          float up[2];  // by how much M moves
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float m = -INFINITY;
+            float m = kNoM;
 #pragma unroll
             for (int sb = 0; sb < SUB; ++sb) m = fmaxf(m, fmaxf(x[sb][nt][c], x[sb][nt][c + 2]));
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-            m = fmaxf(M[nt][c], m - kPOffset);
-            f[c] = ex2(M[nt][c] - m);
-            l[nt][c] *= f[c];
-            M[nt][c] = m;
+            up[c] = step == 0 ? m - kPOffset : fmaxf(m - kPOffset, 0.f);
+            M[nt][c] += up[c];
           }
+#pragma unroll
+          for (int sb = 0; sb < SUB; ++sb)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[sb][nt][c] -= up[c & 1];
+          if (step == 0) continue;  // nothing to rescale yet
+          const float f[2] = {ex2(-up[0]), ex2(-up[1])};
+          l[nt][0] *= f[0], l[nt][1] *= f[1];
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             o[nt][i][0] *= f[0], o[nt][i][1] *= f[1];
@@ -621,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
         for (int nt = 0; nt < NT; ++nt) {
           float pr[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) pr[c] = ex2(x[sb][nt][c] - M[nt][c & 1]);
+          for (int c = 0; c < 4; ++c) pr[c] = ex2(x[sb][nt][c]);
           l[nt][0] = fmaf(pr[0] + pr[2], unit[sb], l[nt][0]);
           l[nt][1] = fmaf(pr[1] + pr[3], unit[sb], l[nt][1]);
           pf[sb][nt][0] = transpose8x8(f2h(pr[0], pr[1]));
@@ -742,12 +752,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT>::kCtasPerSm)
 // that starts in CTA c of the attention kernel: one part in that CTA's slot 1,
 // the others in the following CTAs' slots 0. Few groups have many parts each
 // (long sequences): kSplit gives a CTA one row, its warps every fourth part.
-// Many groups have few parts: then a warp takes a row.
+// Many groups have few parts: then a warp takes a row. It does not let the next
+// kernel start early: CTAs of a following attention kernel that take the places
+// of the first fixup CTAs to end are spread unevenly over the SMs (48 ragged
+// sequences with four CTAs per SM: 101 against 76 us).
 template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads) kv8_fixup_kernel(const AttnArgs a, int heads, int tile_rows) {
   __shared__ float2 wml[kWarps];
   __shared__ float wsum[kWarps][D];
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const Kv8Fix f = a.fix[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -820,17 +832,17 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem
 }
 
 constexpr int kMaxRows = 16;  // query rows of the widest tile
-constexpr int kMaxCtasPerSm = 2;
+constexpr int kMaxCtasPerSm = 3;
 
-template <int D, int SUB, int NT>
+template <int D, int SUB, int NT, int ST>
 cudaError_t launch_attention(AttnArgs a, const Kv8Cache& cache, const Kv8Batch& bt, uint32_t* status,
                              cudaStream_t stream) {
-  using L = Attn<D, SUB, NT>;
+  using L = Attn<D, SUB, NT, ST>;
   static std::atomic<uint64_t> attr_set{0};  // one bit per device that has the attribute
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return cudaErrorInvalidDevice;
   if (!(attr_set.load(std::memory_order_acquire) >> dev & 1)) {
-    cudaError_t e = cudaFuncSetAttribute(kv8_attention_kernel<D, SUB, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kv8_attention_kernel<D, SUB, NT, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(uint64_t(1) << dev, std::memory_order_acq_rel);
   }
@@ -849,7 +861,7 @@ cudaError_t launch_attention(AttnArgs a, const Kv8Cache& cache, const Kv8Batch& 
   }
   a.slot = L::kSlot;
   const int ctas = L::kCtasPerSm * device_info().sm_count;  // all resident: a persistent grid
-  cudaError_t e = launch_pdl(kv8_attention_kernel<D, SUB, NT>, dim3((unsigned)ctas), kThreads, L::kSmem, stream, a, cache, bt, maps[0], maps[1], status);
+  cudaError_t e = launch_pdl(kv8_attention_kernel<D, SUB, NT, ST>, dim3((unsigned)ctas), kThreads, L::kSmem, stream, a, cache, bt, maps[0], maps[1], status);
   if (e != cudaSuccess) return e;
   // groups of units at most; with eight or more parts each, a CTA per row
   const int64_t groups = (int64_t)cache.heads * (bt.seqs + (int64_t)bt.rows * a.group / L::kRows);
@@ -900,11 +912,19 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
   // rows that share a kv head, by the mean of new tokens a sequence (lengths are on the device)
   const int64_t rows = ((int64_t)bt.rows + bt.seqs - 1) / bt.seqs * a.group;
-  if (cache.head_dim == 128)
-    return rows <= 8 ? launch_attention<128, 2, 1>(a, cache, bt, status, stream)
-                     : launch_attention<128, 2, 2>(a, cache, bt, status, stream);
-  return rows <= 8 ? launch_attention<64, 4, 1>(a, cache, bt, status, stream)
-                   : launch_attention<64, 4, 2>(a, cache, bt, status, stream);
+  // Few groups (long sequences) keep one stream per warp: a ring of three steps
+  // and two CTAs per SM. Many groups want more of them under way: two steps
+  // and three CTAs. One sequence of 131002 tokens: 52.8 against 54.5 us; 256
+  // of 20 to 400: 45.4 against 38.4; 16 of 500 to 2047 with 32 kv heads: 39.3
+  // against 36.4. (Several row tiles and 64-wide heads: no such difference.)
+  const bool few = ((int64_t)bt.seqs + bt.rows) * cache.heads * 8 <= 2 * device_info().sm_count;
+  if (cache.head_dim == 128) {
+    if (rows > 8) return launch_attention<128, 2, 2, 3>(a, cache, bt, status, stream);
+    return few ? launch_attention<128, 2, 1, 3>(a, cache, bt, status, stream)
+               : launch_attention<128, 2, 1, 2>(a, cache, bt, status, stream);
+  }
+  return rows <= 8 ? launch_attention<64, 2, 1, 3>(a, cache, bt, status, stream)
+                   : launch_attention<64, 2, 2, 3>(a, cache, bt, status, stream);
 }
 
 }  // namespace awq
