@@ -413,6 +413,10 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
     bool starts, ends;
     int64_t end;  // of the group, in units
   } sg;
+  const bool small = total <= 0x7FFFFFFF;
+  auto divide = [&](int64_t x, int64_t y) -> int64_t {  // a 64-bit division takes as long as a step
+    return small ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+  };
   auto next_segment = [&]() -> bool {
     while (u < u1) {
       Seq s = load_seq(bt, p.b, status);
@@ -423,14 +427,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
         n_seq = row_tiles(s) * (key_tiles(s) + kGroupCost) * cache.heads;
       }
       const int per = key_tiles(s) + kGroupCost;
-      const int64_t in_seq = u - p.base, group_no = in_seq / per;
+      const int64_t in_seq = u - p.base, group_no = divide(in_seq, per);
       const int v0 = (int)(in_seq - group_no * per);
       const int take = (int)(u1 - u < per - v0 ? u1 - u : per - v0);
       sg.tile0 = max(v0 - kGroupCost, 0);
       sg.n = v0 + take - kGroupCost - sg.tile0;
       u += take;
       if (sg.n <= 0) continue;  // only of the units that stand for the group's fixed cost
-      sg.head = (int)(group_no / row_tiles(s));
+      sg.head = (int)divide(group_no, row_tiles(s));
       sg.r0 = (int)(group_no - (int64_t)sg.head * row_tiles(s)) * L::kRows;
       sg.b = p.b;
       sg.row0 = s.row0;
@@ -471,13 +475,13 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
   };
   // Blocks and exponents of the next 32 subtiles, one per lane.
   int blk = -1;
-  float k_exp = 0.f, v_exp = 0.f, k_exp_prev = 0.f, v_exp_prev = 0.f;  // scale log2(e) 2^e_k; e_v
+  int k_exp = 0, v_exp = 0, k_exp_prev = 0, v_exp_prev = 0;
   auto load_info = [&](int sub0) {
     const int sub = sub0 + lane, key = key00 + sub / SUB * L::kKeys + (sub % SUB) * 16;
     k_exp_prev = k_exp;
     v_exp_prev = v_exp;
     blk = -1;
-    k_exp = v_exp = 0.f;
+    k_exp = v_exp = 0;
     if (sub < steps * SUB && key < sg.seen) {
       blk = bt.table[(int64_t)sg.b * bt.table_width + (key >> shift)];
       if (blk < 0 || blk >= cache.blocks) {
@@ -485,8 +489,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
         blk = -1;
       } else {
         const int64_t at = (int64_t)blk * cache.heads + sg.head;
-        k_exp = a.scale_log2 * __int_as_float(((int)cache.k_exp[at] + 127) << 23);
-        v_exp = (float)cache.v_exp[at];
+        k_exp = cache.k_exp[at];  // used no sooner than the step's copies have landed
+        v_exp = cache.v_exp[at];
       }
     }
   };
@@ -545,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
       const int key0 = key00 + step * L::kKeys;
       // the issuing side is up to kStages - 1 steps ahead: it may have loaded the next 32 already
       const bool same = (step * SUB) / 32 == min(step + L::kStages - 1, steps - 1) * SUB / 32;
-      const float k_of = same ? k_exp : k_exp_prev, v_of = same ? v_exp : v_exp_prev;
+      const float k_of = a.scale_log2 * __int_as_float(((same ? k_exp : k_exp_prev) + 127) << 23);
+      const float v_of = (float)(same ? v_exp : v_exp_prev);
 
       // The weights' exponents x + e_v - M of the step's keys (masked keys: -inf)
       float x[SUB][NT][4], unit[SUB];  // unit: 2^-e_v
