@@ -494,22 +494,30 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
       }
     }
   };
-  // The boxes of a step: min(block, step) tokens each. A box of a block that
-  // is not there starts behind the cache's last row, which reads as zeros.
-  const int box = min(bs, 16 * SUB);
+  // The boxes of a step's K and V: 32 tokens each, or two of 16 where that is
+  // the block. A box of a block that is not there starts behind the cache's last
+  // row, which reads as zeros. Issuing takes the elected lane about 190 cycles a
+  // box: a quarter of a step. (A warp of its own for it falls behind on small
+  // blocks, and four of them leave the others too few registers.)
+  static_assert(SUB == 2, "a step is 32 keys");
+  const bool two = bs == 16;
   auto issue = [&](int step) {
     if (step >= steps) return;
     if ((step * SUB) % 32 == 0) load_info(step * SUB);
     const uint32_t bar = bars + 8 * fill, dst = ring + fill * L::kStageBytes;
     fill = fill == L::kStages - 1 ? 0 : fill + 1;
+    const int key = key00 + step * L::kKeys;
+    const int id0 = __shfl_sync(0xffffffffu, blk, step * SUB), id1 = __shfl_sync(0xffffffffu, blk, step * SUB + 1);
+    const int row0 = id0 < 0 ? a.cache_rows : (id0 * cache.heads + sg.head) * bs + (key & (bs - 1));
+    const int row1 = id1 < 0 ? a.cache_rows : (id1 * cache.heads + sg.head) * bs;
     __syncwarp();  // every lane has read what the stage held
-    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
-    for (int i = 0; i < 16 * SUB; i += box) {
-      const int id = __shfl_sync(0xffffffffu, blk, step * SUB + i / 16);
-      const int row = id < 0 ? a.cache_rows : (id * cache.heads + sg.head) * bs + ((key00 + step * L::kKeys + i) & (bs - 1));
-      if (lane == 0) {
-        ptx::tma_load_2d(dst + i * D, &kmap, 0, row, bar);
-        ptx::tma_load_2d(dst + L::kPartBytes + i * D, &vmap, 0, row, bar);
+    if (ptx::elect_one()) {
+      ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
+      ptx::tma_load_2d(dst, &kmap, 0, row0, bar);
+      ptx::tma_load_2d(dst + L::kPartBytes, &vmap, 0, row0, bar);
+      if (two) {
+        ptx::tma_load_2d(dst + 16 * D, &kmap, 0, row1, bar);
+        ptx::tma_load_2d(dst + L::kPartBytes + 16 * D, &vmap, 0, row1, bar);
       }
     }
   };
