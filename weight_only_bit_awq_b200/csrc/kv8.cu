@@ -158,8 +158,8 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
   __shared__ int64_t scan[kWarps];
   __shared__ Place place;
   __shared__ uint32_t wmax[2][kWarps];
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   const int bs = bt.block_tokens, shift = __ffs(bs) - 1, D = cache.head_dim;
   // blocks of sequence b that get new tokens
   auto items = [&](int b) -> int64_t {
@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
     ptx::prefetch_tensormap(&kmap);
     ptx::prefetch_tensormap(&vmap);
   }
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int bs = bt.block_tokens, shift = __ffs(bs) - 1;

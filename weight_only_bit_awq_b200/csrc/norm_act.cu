@@ -110,8 +110,8 @@ __device__ __forceinline__ float norm_factor(const NormArgs& a, int64_t row, flo
 template <int V, bool kRes, bool kFp8>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
   __shared__ uint2 red[64];
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   const int NT = blockDim.x, tid = threadIdx.x;
   uint4 w[V];
 #pragma unroll
@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
 template <bool kRes, bool kFp8>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
   __shared__ uint2 red[64];
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
     const int64_t base = row * a.K8;
@@ -237,8 +237,8 @@ __device__ __forceinline__ void silu8(const uint4& vg, const uint4& vu, float (&
 // fp16 output: no reduction, a CTA takes blockDim * V vectors of one row.
 template <int V>
 __global__ void __launch_bounds__(256) silu_mul_kernel(const SiluArgs a) {
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   const int64_t row = blockIdx.x / (unsigned)a.row_ctas;
   const int c0 = (int)(blockIdx.x - row * a.row_ctas) * blockDim.x * V + threadIdx.x;
   const uint4* g = reinterpret_cast<const uint4*>(a.gu) + row * 2 * a.F8;
@@ -270,8 +270,8 @@ __device__ __forceinline__ float silu_factor(const SiluArgs& a, int64_t row, uin
 template <int V>
 __global__ void __launch_bounds__(1024) silu_mul_fp8_kernel(const SiluArgs a) {
   __shared__ uint2 red[64];
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   const int NT = blockDim.x, tid = threadIdx.x;
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
@@ -304,8 +304,8 @@ __global__ void __launch_bounds__(1024) silu_mul_fp8_kernel(const SiluArgs a) {
 // E4M3 output of rows too long for the registers of one CTA: read twice.
 __global__ void __launch_bounds__(1024) silu_mul_fp8_long_kernel(const SiluArgs a) {
   __shared__ uint2 red[64];
-  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
     const uint4* g = reinterpret_cast<const uint4*>(a.gu) + row * 2 * a.F8;
