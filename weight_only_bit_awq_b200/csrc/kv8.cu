@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
 //
 // Bound by HBM: every code is read once, 4 flops a code and row. Each warp has
 // a ring of its own in shared memory, filled by TMA boxes of whole tokens that
-// its first lane asks for; warps never wait for one another within a segment.
+// it asks for itself; warps never wait for one another within a segment, and
+// the next segment's first copies start before a segment's parts are merged.
 // The boxes are swizzled by 16-byte pieces, so that ldmatrix, which takes one
 // piece of 8 tokens at a time, has no bank conflicts. As 16-bit elements those
 // pieces are pairs of codes: for K, lane (g, t) gets channels 4t .. 4t + 3 of
@@ -288,8 +289,9 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
 // subnormals begin 2^-26 below the largest weight. p is rounded to fp16 (2^-11
 // relative) for the second MMA; l sums the unrounded p.
 constexpr float kPOffset = 12.f, kPMost = 15.f;
-// A group of units costs about as much again as this many units: its q, its
-// first copies' latency, the merge of the warps' parts.
+// A group costs about as much as this many units more: its q, its first copies'
+// latency, the merge of the warps' parts. CTAs get equal ranges of units with
+// these counted (48 ragged sequences: 85 us without, 72 us with two).
 constexpr int kGroupCost = 2;
 constexpr float kNoM = -1e30f;  // M of a row that has seen no key: far below any x, finite
 
@@ -335,15 +337,18 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t a, uint32_t (&r)[4]) {
                : "memory");
 }
 
-// D: head dimension; SUB: 16-key subtiles of a warp's step; NT: column tiles
-// of 8 query rows; ST: steps in a warp's ring. A unit of work is 4 warps x 16 SUB keys of one (sequence,
-// kv head, row tile).
-template <int D, int SUB, int NT, int ST>
+// A step of a warp is two 16-key subtiles; a unit of work, the same step of the
+// four warps, is 128 keys of one group (sequence, kv head, row tile).
+constexpr int kSub = 2;
+constexpr int kStepKeys = 16 * kSub;
+constexpr int kUnitKeys = kWarps * kStepKeys;
+
+// D: head dimension; NT: column tiles of 8 query rows; ST: steps in a warp's ring.
+template <int D, int NT, int ST>
 struct Attn {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kKeys = kWarps * 16 * SUB;             // keys of a unit
   static constexpr int kStages = ST;
-  static constexpr int kPartBytes = SUB * 16 * D;             // a warp's step of K, or of V
+  static constexpr int kPartBytes = kStepKeys * D;            // a warp's step of K, or of V
   static constexpr int kStageBytes = 2 * kPartBytes;
   static_assert(kStageBytes >= kRows * D * 4, "a warp's part of the output fits a stage");
   static constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;  // room to align
@@ -351,12 +356,12 @@ struct Attn {
   static constexpr int kCtasPerSm = kStages * kStageBytes <= 16384 ? 3 : 2;  // by shared memory and registers
 };
 
-template <int D, int SUB, int NT, int ST>
-__global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
+template <int D, int NT, int ST>
+__global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     kv8_attention_kernel(const AttnArgs a, const Kv8Cache cache, const Kv8Batch bt,
                          const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          uint32_t* status) {
-  using L = Attn<D, SUB, NT, ST>;
+  using L = Attn<D, NT, ST>;
   constexpr int KS = D / 16;     // k-steps of S
   constexpr int MT = D / 16;     // channel tiles of O
   extern __shared__ char smem_raw[];
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
   const int bs = bt.block_tokens, shift = __ffs(bs) - 1;
   auto row_tiles = [&](const Seq& s) { return ((int64_t)s.tokens * a.group + L::kRows - 1) / L::kRows; };
   // a sequence with no keys still has one (empty) unit per row tile: its rows are zero
-  auto key_tiles = [&](const Seq& s) { return max((s.len + L::kKeys - 1) / L::kKeys, 1); };
+  auto key_tiles = [&](const Seq& s) { return max((s.len + kUnitKeys - 1) / kUnitKeys, 1); };
   auto items = [&](int b) -> int64_t {
     const Seq s = load_seq(bt, b, status);
     return row_tiles(s) * (key_tiles(s) + kGroupCost) * cache.heads;
@@ -470,19 +475,19 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
   // ---- the warp's steps of a segment
   int key00, steps;  // first key, steps with keys that some row sees
   auto begin_steps = [&]() {
-    key00 = sg.tile0 * L::kKeys + warp * 16 * SUB;
-    steps = sg.seen > key00 ? min((sg.seen - key00 + L::kKeys - 1) / L::kKeys, sg.n) : 0;
+    key00 = sg.tile0 * kUnitKeys + warp * kStepKeys;
+    steps = sg.seen > key00 ? min((sg.seen - key00 + kUnitKeys - 1) / kUnitKeys, sg.n) : 0;
   };
   // Blocks and exponents of the next 32 subtiles, one per lane.
   int blk = -1;
   int k_exp = 0, v_exp = 0, k_exp_prev = 0, v_exp_prev = 0;
   auto load_info = [&](int sub0) {
-    const int sub = sub0 + lane, key = key00 + sub / SUB * L::kKeys + (sub % SUB) * 16;
+    const int sub = sub0 + lane, key = key00 + sub / kSub * kUnitKeys + (sub % kSub) * 16;
     k_exp_prev = k_exp;
     v_exp_prev = v_exp;
     blk = -1;
     k_exp = v_exp = 0;
-    if (sub < steps * SUB && key < sg.seen) {
+    if (sub < steps * kSub && key < sg.seen) {
       blk = bt.table[(int64_t)sg.b * bt.table_width + (key >> shift)];
       if (blk < 0 || blk >= cache.blocks) {
         record_status(status, AWQ_ERR_BOUNDS);
@@ -499,15 +504,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
   // row, which reads as zeros. Issuing takes the elected lane about 190 cycles a
   // box: a quarter of a step. (A warp of its own for it falls behind on small
   // blocks, and four of them leave the others too few registers.)
-  static_assert(SUB == 2, "a step is 32 keys");
   const bool two = bs == 16;
   auto issue = [&](int step) {
     if (step >= steps) return;
-    if ((step * SUB) % 32 == 0) load_info(step * SUB);
+    if ((step * kSub) % 32 == 0) load_info(step * kSub);
     const uint32_t bar = bars + 8 * fill, dst = ring + fill * L::kStageBytes;
     fill = fill == L::kStages - 1 ? 0 : fill + 1;
-    const int key = key00 + step * L::kKeys;
-    const int id0 = __shfl_sync(0xffffffffu, blk, step * SUB), id1 = __shfl_sync(0xffffffffu, blk, step * SUB + 1);
+    const int key = key00 + step * kUnitKeys;
+    const int id0 = __shfl_sync(0xffffffffu, blk, step * kSub), id1 = __shfl_sync(0xffffffffu, blk, step * kSub + 1);
     const int row0 = id0 < 0 ? a.cache_rows : (id0 * cache.heads + sg.head) * bs + (key & (bs - 1));
     const int row1 = id1 < 0 ? a.cache_rows : (id1 * cache.heads + sg.head) * bs;
     __syncwarp();  // every lane has read what the stage held
@@ -554,22 +558,22 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
       const uint32_t src = ring + stage * L::kStageBytes + lane_off;
       stage = stage == L::kStages - 1 ? 0 : stage + 1;
       parity ^= stage == 0;
-      const int key0 = key00 + step * L::kKeys;
+      const int key0 = key00 + step * kUnitKeys;
       // the issuing side is up to kStages - 1 steps ahead: it may have loaded the next 32 already
-      const bool same = (step * SUB) / 32 == min(step + L::kStages - 1, steps - 1) * SUB / 32;
+      const bool same = (step * kSub) / 32 == min(step + L::kStages - 1, steps - 1) * kSub / 32;
       const float k_of = a.scale_log2 * __int_as_float(((same ? k_exp : k_exp_prev) + 127) << 23);
       const float v_of = (float)(same ? v_exp : v_exp_prev);
 
       // The weights' exponents x + e_v - M of the step's keys (masked keys: -inf)
-      float x[SUB][NT][4], unit[SUB];  // unit: 2^-e_v
+      float x[kSub][NT][4], unit[kSub];  // unit: 2^-e_v
 #pragma unroll
-      for (int sb = 0; sb < SUB; ++sb)
+      for (int sb = 0; sb < kSub; ++sb)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) x[sb][nt][0] = x[sb][nt][1] = x[sb][nt][2] = x[sb][nt][3] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < KS; ks += 2)
 #pragma unroll
-        for (int sb = 0; sb < SUB; ++sb) {
+        for (int sb = 0; sb < kSub; ++sb) {
           uint32_t w[4];  // tokens g and g + 8 of piece ks, then of ks + 1
           ldsm4((src + sb * (16 * D)) ^ (ks << 4), w);
 #pragma unroll
@@ -580,18 +584,18 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
           }
         }
 #pragma unroll
-      for (int sb = 0; sb < SUB; ++sb) {
-        const float k_unit = __shfl_sync(0xffffffffu, k_of, step * SUB + sb);
-        const float ev = __shfl_sync(0xffffffffu, v_of, step * SUB + sb);
+      for (int sb = 0; sb < kSub; ++sb) {
+        const float k_unit = __shfl_sync(0xffffffffu, k_of, step * kSub + sb);
+        const float ev = __shfl_sync(0xffffffffu, v_of, step * kSub + sb);
         unit[sb] = ex2(-ev);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) x[sb][nt][c] = fmaf(x[sb][nt][c], k_unit, ev - M[nt][c & 1]);
       }
-      if (key0 + 16 * SUB > least) {  // some row does not see all of the step's keys
+      if (key0 + kStepKeys > least) {  // some row does not see all of the step's keys
 #pragma unroll
-        for (int sb = 0; sb < SUB; ++sb)
+        for (int sb = 0; sb < kSub; ++sb)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
       // follows its running maximum.
       float over = -INFINITY;
 #pragma unroll
-      for (int sb = 0; sb < SUB; ++sb)
+      for (int sb = 0; sb < kSub; ++sb)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -616,14 +620,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
           for (int c = 0; c < 2; ++c) {
             float m = kNoM;
 #pragma unroll
-            for (int sb = 0; sb < SUB; ++sb) m = fmaxf(m, fmaxf(x[sb][nt][c], x[sb][nt][c + 2]));
+            for (int sb = 0; sb < kSub; ++sb) m = fmaxf(m, fmaxf(x[sb][nt][c], x[sb][nt][c + 2]));
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
             up[c] = step == 0 ? m - kPOffset : fmaxf(m - kPOffset, 0.f);
             M[nt][c] += up[c];
           }
 #pragma unroll
-          for (int sb = 0; sb < SUB; ++sb)
+          for (int sb = 0; sb < kSub; ++sb)
 #pragma unroll
             for (int c = 0; c < 4; ++c) x[sb][nt][c] -= up[c & 1];
           if (step == 0) continue;  // nothing to rescale yet
@@ -637,9 +641,9 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
         }
       }
 
-      uint32_t pf[SUB][NT][2];
+      uint32_t pf[kSub][NT][2];
 #pragma unroll
-      for (int sb = 0; sb < SUB; ++sb)
+      for (int sb = 0; sb < kSub; ++sb)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float pr[4];
@@ -651,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, SUB, NT, ST>::kCtasPerSm)
           pf[sb][nt][1] = transpose8x8(f2h(pr[2], pr[3]));
         }
 #pragma unroll
-      for (int sb = 0; sb < SUB; ++sb) {
+      for (int sb = 0; sb < kSub; ++sb) {
         const int key = key0 + 16 * sb;
 #pragma unroll
         for (int i = 0; i < MT; i += 2) {
@@ -847,15 +851,15 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem
 constexpr int kMaxRows = 16;  // query rows of the widest tile
 constexpr int kMaxCtasPerSm = 3;
 
-template <int D, int SUB, int NT, int ST>
+template <int D, int NT, int ST>
 cudaError_t launch_attention(AttnArgs a, const Kv8Cache& cache, const Kv8Batch& bt, uint32_t* status,
                              cudaStream_t stream) {
-  using L = Attn<D, SUB, NT, ST>;
+  using L = Attn<D, NT, ST>;
   static std::atomic<uint64_t> attr_set{0};  // one bit per device that has the attribute
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return cudaErrorInvalidDevice;
   if (!(attr_set.load(std::memory_order_acquire) >> dev & 1)) {
-    cudaError_t e = cudaFuncSetAttribute(kv8_attention_kernel<D, SUB, NT, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kv8_attention_kernel<D, NT, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(uint64_t(1) << dev, std::memory_order_acq_rel);
   }
@@ -863,7 +867,7 @@ cudaError_t launch_attention(AttnArgs a, const Kv8Cache& cache, const Kv8Batch& 
   for (int i = 0; i < 2; ++i) {
     const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)a.cache_rows};
     const cuuint64_t strides[1] = {(cuuint64_t)D};
-    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)(bt.block_tokens < 16 * SUB ? bt.block_tokens : 16 * SUB)};
+    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)(bt.block_tokens < kStepKeys ? bt.block_tokens : kStepKeys)};
     const cuuint32_t estr[2] = {1, 1};
     auto encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
@@ -874,7 +878,7 @@ cudaError_t launch_attention(AttnArgs a, const Kv8Cache& cache, const Kv8Batch& 
   }
   a.slot = L::kSlot;
   const int ctas = L::kCtasPerSm * device_info().sm_count;  // all resident: a persistent grid
-  cudaError_t e = launch_pdl(kv8_attention_kernel<D, SUB, NT, ST>, dim3((unsigned)ctas), kThreads, L::kSmem, stream, a, cache, bt, maps[0], maps[1], status);
+  cudaError_t e = launch_pdl(kv8_attention_kernel<D, NT, ST>, dim3((unsigned)ctas), kThreads, L::kSmem, stream, a, cache, bt, maps[0], maps[1], status);
   if (e != cudaSuccess) return e;
   // groups of units at most; with eight or more parts each, a CTA per row
   const int64_t groups = (int64_t)cache.heads * (bt.seqs + (int64_t)bt.rows * a.group / L::kRows);
@@ -932,12 +936,12 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
   // against 36.4. (Several row tiles and 64-wide heads: no such difference.)
   const bool few = ((int64_t)bt.seqs + bt.rows) * cache.heads * 8 <= 2 * device_info().sm_count;
   if (cache.head_dim == 128) {
-    if (rows > 8) return launch_attention<128, 2, 2, 3>(a, cache, bt, status, stream);
-    return few ? launch_attention<128, 2, 1, 3>(a, cache, bt, status, stream)
-               : launch_attention<128, 2, 1, 2>(a, cache, bt, status, stream);
+    if (rows > 8) return launch_attention<128, 2, 3>(a, cache, bt, status, stream);
+    return few ? launch_attention<128, 1, 3>(a, cache, bt, status, stream)
+               : launch_attention<128, 1, 2>(a, cache, bt, status, stream);
   }
-  return rows <= 8 ? launch_attention<64, 2, 1, 3>(a, cache, bt, status, stream)
-                   : launch_attention<64, 2, 2, 3>(a, cache, bt, status, stream);
+  return rows <= 8 ? launch_attention<64, 1, 3>(a, cache, bt, status, stream)
+                   : launch_attention<64, 2, 3>(a, cache, bt, status, stream);
 }
 
 }  // namespace awq
