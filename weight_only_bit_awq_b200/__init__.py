@@ -20,6 +20,7 @@ Functions (same names as the C entry points):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -297,13 +298,19 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
+@functools.cache
+def _device_count() -> int:
+    return torch.cuda.device_count()
+
+
 def _call(fn, name: str, tensors, *args):
     """fn(*args, stream) on the device of the tensors (which must share one),
     on that device's current stream."""
     device = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != device:
-            raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
+    if _device_count() > 1:  # every tensor is known to be on a GPU
+        for t in tensors:
+            if t.get_device() != device:
+                raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
     if device == _current_device():
         status = fn(*args, _raw_stream(device))
     else:

@@ -293,6 +293,11 @@ constexpr float kPOffset = 12.f, kPMost = 15.f;
 // latency, the merge of the warps' parts. CTAs get equal ranges of units with
 // these counted (48 ragged sequences: 85 us without, 72 us with two).
 constexpr int kGroupCost = 2;
+// Where the block table holds no more keys than this, a CTA takes whole groups
+// and there is no fixup kernel: one sequence of 128 / 512 / 1024 tokens 5.7 /
+// 8.4 / 12.1 us against 7.6 / 8.2 / 8.7 us split, 32 sequences of 256 to 512
+// tokens 8.0 to 8.8 against 10.6 to 11.6 us, and a launch less to wait for.
+constexpr int kWholeKeys = 512;
 constexpr float kNoM = -1e30f;  // M of a row that has seen no key: far below any x, finite
 
 // The group of units that starts in a CTA's range and ends in a later one's.
@@ -310,6 +315,7 @@ struct AttnArgs {
   int slot;           // floats of a slot: rows * (D + 2)
   Kv8Fix* fix;        // [ctas]
   int cache_rows;     // blocks * heads * block_tokens
+  bool whole;         // groups are not split between CTAs
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -388,9 +394,11 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   auto row_tiles = [&](const Seq& s) { return ((int64_t)s.tokens * a.group + L::kRows - 1) / L::kRows; };
   // a sequence with no keys still has one (empty) unit per row tile: its rows are zero
   auto key_tiles = [&](const Seq& s) { return max((s.len + kUnitKeys - 1) / kUnitKeys, 1); };
+  // what a group of the sequence counts in the split
+  auto group_units = [&](const Seq& s) { return a.whole ? 1 : key_tiles(s) + kGroupCost; };
   auto items = [&](int b) -> int64_t {
     const Seq s = load_seq(bt, b, status);
-    return row_tiles(s) * (key_tiles(s) + kGroupCost) * cache.heads;
+    return row_tiles(s) * group_units(s) * cache.heads;
   };
   int64_t before;
   const int64_t total = total_items(bt.seqs, items, scan, before);
@@ -425,18 +433,18 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   auto next_segment = [&]() -> bool {
     while (u < u1) {
       Seq s = load_seq(bt, p.b, status);
-      int64_t n_seq = row_tiles(s) * (key_tiles(s) + kGroupCost) * cache.heads;
+      int64_t n_seq = row_tiles(s) * group_units(s) * cache.heads;
       while (u >= p.base + n_seq) {
         p.base += n_seq;
         s = load_seq(bt, ++p.b, status);
-        n_seq = row_tiles(s) * (key_tiles(s) + kGroupCost) * cache.heads;
+        n_seq = row_tiles(s) * group_units(s) * cache.heads;
       }
-      const int per = key_tiles(s) + kGroupCost;
+      const int per = group_units(s);
       const int64_t in_seq = u - p.base, group_no = divide(in_seq, per);
       const int v0 = (int)(in_seq - group_no * per);
       const int take = (int)(u1 - u < per - v0 ? u1 - u : per - v0);
       sg.tile0 = max(v0 - kGroupCost, 0);
-      sg.n = v0 + take - kGroupCost - sg.tile0;
+      sg.n = a.whole ? key_tiles(s) : v0 + take - kGroupCost - sg.tile0;
       u += take;
       if (sg.n <= 0) continue;  // only of the units that stand for the group's fixed cost
       sg.head = (int)divide(group_no, row_tiles(s));
@@ -879,7 +887,7 @@ cudaError_t launch_attention(AttnArgs a, const Kv8Cache& cache, const Kv8Batch& 
   a.slot = L::kSlot;
   const int ctas = L::kCtasPerSm * device_info().sm_count;  // all resident: a persistent grid
   cudaError_t e = launch_pdl(kv8_attention_kernel<D, NT, ST>, dim3((unsigned)ctas), kThreads, L::kSmem, stream, a, cache, bt, maps[0], maps[1], status);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.whole) return e;
   // groups of units at most; with eight or more parts each, a CTA per row
   const int64_t groups = (int64_t)cache.heads * (bt.seqs + (int64_t)bt.rows * a.group / L::kRows);
   if (groups * 8 <= ctas)
@@ -924,6 +932,7 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
   a.group = q_heads / cache.heads;
   a.scale_log2 = scale * kLog2e;
   a.cache_rows = (int)(cache.blocks * cache.heads * bt.block_tokens);
+  a.whole = (int64_t)bt.table_width * bt.block_tokens <= kWholeKeys;
   a.fix = reinterpret_cast<Kv8Fix*>(ws + kWsHeaderBytes);
   a.partial = reinterpret_cast<float*>(ws + kWsHeaderBytes + ctas * sizeof(Kv8Fix));
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
