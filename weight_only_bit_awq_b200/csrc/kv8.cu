@@ -11,6 +11,7 @@
 #include <cuda_fp8.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "awq_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -293,10 +294,12 @@ constexpr float kPOffset = 12.f, kPMost = 15.f;
 // latency, the merge of the warps' parts. CTAs get equal ranges of units with
 // these counted (48 ragged sequences: 85 us without, 72 us with two).
 constexpr int kGroupCost = 2;
-// Where the block table holds no more keys than this, a CTA takes whole groups
-// and there is no fixup kernel: one sequence of 128 / 512 / 1024 tokens 5.7 /
+// Where the block table holds no more keys than this, and the groups are not
+// many times the CTAs, a CTA takes whole groups and there is no fixup kernel:
+// one sequence of 128 / 512 / 1024 tokens 5.7 /
 // 8.4 / 12.1 us against 7.6 / 8.2 / 8.7 us split, 32 sequences of 256 to 512
-// tokens 8.0 to 8.8 against 10.6 to 11.6 us, and a launch less to wait for.
+// tokens 8.0 to 8.8 against 10.6 to 11.6 us, and a launch less to wait for (but
+// 256 sequences of 20 to 400: 38.8 against 36.5 us).
 constexpr int kWholeKeys = 512;
 constexpr float kNoM = -1e30f;  // M of a row that has seen no key: far below any x, finite
 
@@ -662,54 +665,62 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
           pf[sb][nt][0] = transpose8x8(f2h(pr[0], pr[1]));
           pf[sb][nt][1] = transpose8x8(f2h(pr[2], pr[3]));
         }
+      // O += V^T P^T. Where a row does not see all 16 keys of a subtile, a NaN
+      // code must reach only the rows that see it: 0 * NaN in the MMA would
+      // reach all. Such codes are taken out there, and their channels of the
+      // rows that see them set to NaN. (Places behind the end can hold NaN codes
+      // too.) The other steps have no branch between their loads.
+      auto add_pv = [&](auto careful) {
 #pragma unroll
-      for (int sb = 0; sb < kSub; ++sb) {
-        const int key = key0 + 16 * sb;
+        for (int sb = 0; sb < kSub; ++sb) {
+          const int key = key0 + 16 * sb;
 #pragma unroll
-        for (int i = 0; i < MT; i += 2) {
-          uint32_t w[4];  // channels 2g, 2g + 1 of piece i: tokens 2t, 2t + 1, then + 8; the same of piece i + 1
-          ldsm4_trans((src + L::kPartBytes + sb * (16 * D)) ^ (i << 4), w);
-          // Where a row does not see all 16 keys, a NaN code must reach only
-          // the rows that see it: 0 * NaN in the MMA would reach all. Such
-          // codes are taken out, and their channels of the rows that see them
-          // set to NaN here. (Places behind the end can hold NaN codes too.)
-          if (key + 16 > least) {
-            uint32_t nan[4], any = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              nan[j] = ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // 0x80 in bytes that are 0x7F or 0xFF
-              any |= nan[j];
-            }
-            if (__any_sync(0xffffffffu, any)) {
+          for (int i = 0; i < MT; i += 2) {
+            uint32_t w[4];  // channels 2g, 2g + 1 of piece i: tokens 2t, 2t + 1, then + 8; the same of piece i + 1
+            ldsm4_trans((src + L::kPartBytes + sb * (16 * D)) ^ (i << 4), w);
+            if constexpr (decltype(careful)::value) {
+              uint32_t nan[4], any = 0;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                w[j] &= ~((nan[j] >> 7) * 0xFFu);
+                nan[j] = ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // 0x80 in bytes that are 0x7F or 0xFF
+                any |= nan[j];
+              }
+              if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  w[j] &= ~((nan[j] >> 7) * 0xFFu);
 #pragma unroll 1
-                for (int tt = 0; tt < 4; ++tt) {  // the four lanes that share this lane's channels
-                  const uint32_t m = __shfl_sync(0xffffffffu, nan[j], (lane & ~3) | tt);
-                  if (m == 0) continue;
+                  for (int tt = 0; tt < 4; ++tt) {  // the four lanes that share this lane's channels
+                    const uint32_t m = __shfl_sync(0xffffffffu, nan[j], (lane & ~3) | tt);
+                    if (m == 0) continue;
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)  // byte b: token + (b >> 1), channel + (b & 1)
+                      for (int b = 0; b < 4; ++b)  // byte b: token + (b >> 1), channel + (b & 1)
 #pragma unroll
-                      for (int c = 0; c < 2; ++c)
-                        if ((m >> (8 * b + 7) & 1) && key + 2 * tt + 8 * (j & 1) + (b >> 1) < limit[nt][c])
-                          o[nt][i + (j >> 1)][2 * (b & 1) + c] = NAN;
+                        for (int c = 0; c < 2; ++c)
+                          if ((m >> (8 * b + 7) & 1) && key + 2 * tt + 8 * (j & 1) + (b >> 1) < limit[nt][c])
+                            o[nt][i + (j >> 1)][2 * (b & 1) + c] = NAN;
+                  }
                 }
               }
             }
-          }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t p0 = __byte_perm(w[2 * j], 0, 0x3120), p1 = __byte_perm(w[2 * j + 1], 0, 0x3120);
-            const uint32_t a0 = lo_h2(p0), a1 = hi_h2(p0), a2 = lo_h2(p1), a3 = hi_h2(p1);
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t p0 = __byte_perm(w[2 * j], 0, 0x3120), p1 = __byte_perm(w[2 * j + 1], 0, 0x3120);
+              const uint32_t a0 = lo_h2(p0), a1 = hi_h2(p0), a2 = lo_h2(p1), a3 = hi_h2(p1);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i + j], a0, a1, a2, a3, pf[sb][nt][0], pf[sb][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i + j], a0, a1, a2, a3, pf[sb][nt][0], pf[sb][nt][1]);
+            }
           }
         }
-      }
+      };
+      if (key0 + kStepKeys > least)
+        add_pv(std::true_type());
+      else
+        add_pv(std::false_type());
     }
+
     // ---- the next segment's copies start before this one's parts are merged
     const Segment w = sg;
     have = next_segment();
@@ -932,7 +943,9 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
   a.group = q_heads / cache.heads;
   a.scale_log2 = scale * kLog2e;
   a.cache_rows = (int)(cache.blocks * cache.heads * bt.block_tokens);
-  a.whole = (int64_t)bt.table_width * bt.block_tokens <= kWholeKeys;
+  // ("not many": about as many groups as sequences and tokens times kv heads)
+  a.whole = (int64_t)bt.table_width * bt.block_tokens <= kWholeKeys &&
+            ((int64_t)bt.seqs + bt.rows) * cache.heads <= 8 * device_info().sm_count;
   a.fix = reinterpret_cast<Kv8Fix*>(ws + kWsHeaderBytes);
   a.partial = reinterpret_cast<float*>(ws + kWsHeaderBytes + ctas * sizeof(Kv8Fix));
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
