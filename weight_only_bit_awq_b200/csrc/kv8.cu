@@ -110,6 +110,11 @@ __device__ __forceinline__ uint32_t f2h(float a, float b) {
 __device__ __forceinline__ uint32_t code2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
+// The codes of two fp16 values times m.
+__device__ __forceinline__ uint32_t code2_h(uint32_t w, __half2 m) {
+  const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&w), m);
+  return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(p), __NV_SATFINITE, __NV_E4M3);
+}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -227,23 +232,36 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
     if (threadIdx.x == 0) *exps[part] = (int8_t)e;
     uint8_t* dst = (part ? cache.v : cache.k) + at * bs * D + 8 * c;
     const float inv = ldexpf(1.f, -e);
+    if (!odd[part] && e >= -15 && e <= 14) {
+      // 2^-e is an fp16 number, and a product that fp16 does not hold exactly
+      // lies below 2^-14, where every code is zero
+      const __half2 inv2 = __float2half2_rn(inv);
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-      const int r = r0 + i * rows_per_pass;
-      if (r < lo || r >= hi) continue;
-      const uint32_t w[4] = {x[part][i].x, x[part][i].y, x[part][i].z, x[part][i].w};
-      uint32_t o[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float2 f = h2f(w[q]);
-        f.x *= inv, f.y *= inv;  // exact
-        if (odd[part]) {  // the conversion would saturate an infinity
-          if (!(fabsf(f.x) < INFINITY)) f.x = NAN;
-          if (!(fabsf(f.y) < INFINITY)) f.y = NAN;
-        }
-        o[q] = code2(f.x, f.y);
+      for (int i = 0; i < kIter; ++i) {
+        const int r = r0 + i * rows_per_pass;
+        const uint4& v = x[part][i];
+        if (r >= lo && r < hi)
+          *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(code2_h(v.x, inv2) | (code2_h(v.y, inv2) << 16),
+                                                              code2_h(v.z, inv2) | (code2_h(v.w, inv2) << 16));
       }
-      *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+    } else {
+#pragma unroll 1
+      for (int r = r0; r < hi; r += rows_per_pass) {
+        if (r < lo) continue;
+        const __half* s = (part ? vnew + (row0 + r) * v_stride : knew + (row0 + r) * k_stride) + (int64_t)h * D + 8 * c;
+        const uint4 v = *reinterpret_cast<const uint4*>(s);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float2 f = h2f(w[q]);
+          f.x *= inv, f.y *= inv;                 // exact
+          if (!(fabsf(f.x) < INFINITY)) f.x = NAN;  // the conversion would saturate an infinity
+          if (!(fabsf(f.y) < INFINITY)) f.y = NAN;
+          o[q] = code2(f.x, f.y);
+        }
+        *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+      }
     }
     if (e > e_old[part] && lo > 0) {  // the codes that were there, under the larger exponent
       const float down = ldexpf(1.f, e_old[part] - e);
