@@ -428,3 +428,63 @@ def test_offsets_beyond_32_bits():
     bt.append()
     for t, s in zip(big, old):
         assert torch.equal(t[at], s[rows])
+
+
+def test_more_sequences_than_a_grid_dimension_holds():
+    # one token each: the attention returns the value that the cache holds
+    B, D = 70001, 64
+    g = torch.Generator(device="cuda").manual_seed(18)
+    q, k, v = (torch.randn(B, 1, D, generator=g, device="cuda").half() for _ in "qkv")
+    cache = awq.new_kv8_cache(B, 1, 16, D, "cuda")
+    starts = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    table = torch.randperm(B, generator=g, device="cuda").to(torch.int32).view(B, 1)
+    ws = awq.new_kv8_workspace(B, B, 1, 1, D, "cuda")
+    awq.awq_kv8_append(k, v, cache, starts, lens, table, ws)
+    y = awq.awq_kv8_attention(q, cache, starts, lens, table, ws)
+    assert awq.awq_get_status(ws) == awq.AWQ_OK
+    rows = table.view(-1).long()
+    for src, codes, exps in ((k, cache.k, cache.k_exp), (v, cache.v, cache.v_exp)):
+        amax = src.view(B, D).double().abs().amax(dim=1)
+        e = exps[rows].view(B).double()
+        assert (amax <= 448 * torch.exp2(e)).all() and (amax > 448 * torch.exp2(e - 1)).all()
+        assert torch.equal(codes[rows, 0, 0], (src.view(B, D).double() * torch.exp2(-e)[:, None]).float().to(E4M3).view(torch.uint8))
+    held = values(cache.v[rows], cache.v_exp[rows])[:, 0, 0]
+    assert torch.equal(y.double(), held)
+
+
+def test_a_prompt_in_pieces_equals_the_prompt_at_once():
+    # attention of a prompt appended and read in pieces against all of it: the
+    # same tokens see the same keys (the codes differ where a block was filled in
+    # two pieces, so the pieces end on blocks)
+    T, block = 704, 64
+    bt = Batch([T], [T], 8, 2, 128, block, seed=19, empty=True)
+    bt.append()
+    bt.check("prompt")
+    codes = [t.clone() for t in bt.cache]
+    q, k, v = bt.q, bt.k, bt.v
+    for t in bt.cache:
+        t.zero_()
+    at = 0
+    for n in (64, 320, 128, 192):
+        bt.new, bt.R, bt.starts_h = [n], n, [0, n]
+        bt.starts = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        bt.n, bt.lens = [at + n], torch.tensor([at + n], dtype=torch.int32, device="cuda")
+        bt.q, bt.k, bt.v = (x[at:at + n] for x in (q, k, v))
+        bt.append()
+        bt.check("piece")
+        at += n
+    for a, b in zip(bt.cache, codes):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("capacity", [512, 528])
+def test_both_ways_of_sharing_out_the_work(capacity):
+    # the same batch with a block table at and above the size up to which CTAs
+    # take whole groups
+    lens = [1, 16, 130, 512, 500]
+    bt = Batch([1, 1, 2, 1, 3], lens, 16, 2, 64, 16, seed=22)
+    table = torch.full((5, capacity // 16), -1, dtype=torch.int32, device="cuda")
+    table[:, :bt.table.shape[1]] = bt.table
+    bt.table = table
+    bt.check(capacity)

@@ -225,3 +225,25 @@ def test_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(y, want_y) and torch.equal(h, want_h)
         assert torch.equal(x8, want_s[0]) and torch.equal(sx, want_s[1])
+
+
+def test_offsets_beyond_32_bits():
+    # 2^31 + elements in x and y; the last rows are checked
+    K, M = 32768, (1 << 16) + 5
+    free, _ = torch.cuda.mem_get_info()
+    assert free > 24 << 30
+    x = torch.zeros(M, K, dtype=torch.float16, device="cuda")
+    tail = slice(M - 4, M)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x[tail] = torch.randn(4, K, generator=g, device="cuda").half()
+    w = torch.ones(K, device="cuda").half()
+    y = awq.awq_rmsnorm(x, w, EPS)
+    check_fp16(y[tail], norm_ref(x[tail], w, EPS), fp32_slack(K), "norm")
+    del y
+    x8, sx = awq.awq_rmsnorm_fp8(x, w, EPS)
+    check_fp8(x8[tail], sx[tail], norm_ref(x[tail], w, EPS), fp32_slack(K), "norm fp8")
+    del x8
+    rel = 32 * 2.0 ** -23
+    check_fp16(awq.awq_silu_mul(x)[tail], silu_ref(x[tail]), rel, "silu")
+    x8, sx = awq.awq_silu_mul_fp8(x)
+    check_fp8(x8[tail], sx[tail], silu_ref(x[tail]), rel, "silu fp8")

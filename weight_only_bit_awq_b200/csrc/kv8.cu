@@ -76,7 +76,9 @@ struct Place {
   int64_t base;
 };
 
-// Sequence of item u < total; `before` is this thread's from total_items.
+// Sequence of item u < total; `before` is this thread's from total_items, whose
+// caller has set *shared to the first sequence: what is found stays inside the
+// batch even if the lists change while a kernel reads them.
 template <typename Items>
 __device__ __forceinline__ Place find_item(int B, const Items& items, int64_t before, int64_t u, Place* shared) {
   const int per = (B + kThreads - 1) / kThreads;
@@ -173,6 +175,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
     const int first = max(s.len - s.tokens, 0);
     return first < s.len && s.tokens > 0 ? ((s.len - 1) >> shift) - (first >> shift) + 1 : 0;
   };
+  if (threadIdx.x == 0) place = Place{0, 0};
   int64_t before;
   const int64_t total = total_items(bt.seqs, items, scan, before);
   const int64_t u = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
   const Place p = find_item(bt.seqs, items, before, u, &place);
   const Seq s = load_seq(bt, p.b, status);
   const int past = s.len - s.tokens;  // position of the first new row (rows at negative positions have no place)
-  const int j = (max(past, 0) >> shift) + (int)(u - p.base);
+  const int j = min((max(past, 0) >> shift) + (int)(u - p.base), bt.table_width - 1);
   const int h = blockIdx.x;
   const int lo = max(max(past, 0) - j * bs, 0), hi = min(s.len - j * bs, bs);  // new rows of the block
   const int pieces = D / 8, rows_per_pass = kThreads / pieces;
@@ -383,6 +386,14 @@ struct Attn {
   static constexpr int kCtasPerSm = kStages * kStageBytes <= 16384 ? 3 : 2;  // by shared memory and registers
 };
 
+// The part of a group in a CTA's range.
+struct Segment {
+  int b, row0, len, past, rows, r0, head, tile0, n;
+  int seen;     // keys that some row sees
+  bool starts, ends;
+  int64_t end;  // of the group, in units
+};
+
 template <int D, int NT, int ST>
 __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     kv8_attention_kernel(const AttnArgs a, const Kv8Cache cache, const Kv8Batch bt,
@@ -399,6 +410,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   __shared__ uint32_t abort_word;
   __shared__ float2 ml[kWarps][L::kRows];  // M and l of the warps' rows
   __shared__ const float* parts[kWarps];
+  __shared__ Segment ahead[2];
+  __shared__ int ahead_valid[2];
   volatile uint32_t* const abort_flag = &abort_word;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWarps * L::kStages; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
@@ -421,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     const Seq s = load_seq(bt, b, status);
     return row_tiles(s) * group_units(s) * cache.heads;
   };
+  if (threadIdx.x == 0) place = Place{0, 0};
   int64_t before;
   const int64_t total = total_items(bt.seqs, items, scan, before);
   const int64_t ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
@@ -440,22 +454,20 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   int stage = 0, fill = 0;   // ring positions of the next step to use and to fill
   uint32_t parity = 0;
 
-  // ---- segments: the parts of groups in this CTA's range
-  struct Segment {
-    int b, row0, len, past, rows, r0, head, tile0, n;
-    int seen;     // keys that some row sees
-    bool starts, ends;
-    int64_t end;  // of the group, in units
-  } sg;
+  // ---- segments: the parts of groups in this CTA's range. The first warp walks
+  // the batch one segment ahead and hands them out, so that all warps take the
+  // same steps even if the lists change under them.
+  Segment sg;
   const bool small = total <= 0x7FFFFFFF;
   auto divide = [&](int64_t x, int64_t y) -> int64_t {  // a 64-bit division takes as long as a step
     return small ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
   };
-  auto next_segment = [&]() -> bool {
+  auto next_segment = [&](Segment& sg) -> bool {
     while (u < u1) {
       Seq s = load_seq(bt, p.b, status);
       int64_t n_seq = row_tiles(s) * group_units(s) * cache.heads;
       while (u >= p.base + n_seq) {
+        if (p.b + 1 >= bt.seqs) return false;
         p.base += n_seq;
         s = load_seq(bt, ++p.b, status);
         n_seq = row_tiles(s) * group_units(s) * cache.heads;
@@ -482,6 +494,16 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
       return true;
     }
     return false;
+  };
+
+  auto hand_out = [&](int slot) {
+    if (warp != 0) return;
+    Segment s;
+    const bool more = next_segment(s);
+    if (lane == 0) {
+      ahead[slot] = s;
+      ahead_valid[slot] = more;
+    }
   };
 
   // ---- a segment's query rows as B fragments, channels in K's order
@@ -562,9 +584,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   };
 
   bool dead = false;  // a wait gave up: no more copies, the results are garbage
-  bool have = next_segment();
+  hand_out(0);
+  __syncthreads();
+  bool have = ahead_valid[0];
+  sg = ahead[0];
   if (have) begin_segment();
-  while (have) {
+  hand_out(1);
+  bool first = true;
+  for (int turn = 0; have; turn ^= 1) {
     int limit[NT][2];  // keys that the lane's two rows of each column tile see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -741,7 +768,10 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
 
     // ---- the next segment's copies start before this one's parts are merged
     const Segment w = sg;
-    have = next_segment();
+    if (first) __syncthreads();  // the second segment is there (later ones: a merge's barrier)
+    first = false;
+    have = ahead_valid[turn ^ 1];
+    sg = ahead[turn ^ 1];
     if (have && !dead) begin_segment();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -792,8 +822,9 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
       }
     }
     if (w.starts && !w.ends && tid == 0)  // the CTA that holds the group's last unit: the last c with first_unit(c) < its end
-      a.fix[blockIdx.x] = Kv8Fix{1, w.row0, w.rows, w.r0, w.head, (int)((w.end * ctas + total - 1) / total) - 1, 0, 0};
+      a.fix[blockIdx.x] = Kv8Fix{1, w.row0, w.rows, w.r0, w.head, (int)min((w.end * ctas + total - 1) / total, ctas) - 1, 0, 0};
     ptx::fence_proxy_async_smem();  // copies will come where the parts were
+    hand_out(turn);
     if (__syncthreads_or(dead)) break;
   }
   // After a timeout, copies still on their way must land before this CTA is gone.
