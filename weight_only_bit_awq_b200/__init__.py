@@ -360,7 +360,7 @@ def awq_rmsnorm_fp8(x, weight, eps: float, residual=None, h=None, x8=None, sx=No
     """awq_rmsnorm with y as (x8 uint8 E4M3 codes [M][K], sx float32 [M]), the
     inputs of awq_w4a8_gemm; (x8, sx, h) with a residual."""
     M, K, tensors, px, pr, pw, h = _norm_inputs(x, weight, residual, h)
-    x8 = x.new_empty((M, K), dtype=torch.uint8) if x8 is None else _given(x8, (M, K), torch.uint8, "x8")
+    x8 = torch.empty_like(x, dtype=torch.uint8) if x8 is None else _given(x8, (M, K), torch.uint8, "x8")
     sx = x.new_empty(M, dtype=torch.float32) if sx is None else _given(sx, (M,), torch.float32, "sx")
     _call(lib.awq_rmsnorm_fp8, "awq_rmsnorm_fp8", tensors + [x8, sx], px, pr, pw, eps,
           None if h is None else h.data_ptr(), x8.data_ptr(), sx.data_ptr(), M, K)
