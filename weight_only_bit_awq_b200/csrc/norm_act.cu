@@ -108,57 +108,74 @@ __device__ __forceinline__ float norm_factor(const NormArgs& a, int64_t row, flo
   return mx > 0.f ? kE4m3Max / mx : 0.f;
 }
 
-// One CTA a row at a time, the row in V vectors of 8 per thread. The fp16 form
-// takes the weights only after the reduction: 32 registers a thread then keep
-// two CTAs of 1024 threads on an SM (517 x 14848: 7.5 against 9.9 us).
-template <int V, bool kRes, bool kFp8>
-__global__ void __launch_bounds__(1024, V == 2 && !kFp8 ? 2 : 1) rmsnorm_kernel(const NormArgs a) {
+// One CTA a row at a time, the row in V vectors of 8 per thread. The weights are
+// read for each row (from L1) rather than kept. kWide: more than 512 threads;
+// with 32 registers a thread two such CTAs fit an SM (517 x 14848 to fp16 7.5
+// against 9.9 us with one, 4096 x 11008 to E4M3 50.2 against 60.1, x 14848 73.5
+// against 72.2; narrower CTAs lose by that limit: 8192 x 8192 to E4M3 78.2
+// against 72.0).
+// With four vectors a thread there is one CTA on an SM, so nothing would be
+// loaded while it computes: there the next row's inputs are copied to shared
+// memory meanwhile, by the threads that will use them, so that needs no barrier
+// (2048 x 28672 to E4M3: 66.6 against 71.5 us; 8192 wide 80.9 against 73.1).
+template <int V, bool kRes, bool kFp8, bool kWide>
+__global__ void __launch_bounds__(kWide ? 1024 : 512, V <= 2 ? 2 : 1) rmsnorm_kernel(const NormArgs a) {
+  constexpr bool kAhead = V == 4;
+  extern __shared__ uint4 ahead[];  // [V][x, residual][thread]
   __shared__ uint2 red[64];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int NT = blockDim.x, tid = threadIdx.x;
-  uint4 w[V];
-  if (kFp8) {
+  constexpr int kIn = kRes ? 2 : 1;
+  const uint4 *x = reinterpret_cast<const uint4*>(a.x), *residual = reinterpret_cast<const uint4*>(a.residual);
+  auto copy = [&](int64_t row) {
+    if (row >= a.M) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * NT + tid;
-      w[i] = c < a.K8 ? reinterpret_cast<const uint4*>(a.w)[c] : make_uint4(0, 0, 0, 0);
+      if (c >= a.K8) continue;
+      ptx::cp_async_16(ptx::smem_u32(ahead + kIn * i * NT + tid), x + row * a.K8 + c);
+      if (kRes) ptx::cp_async_16(ptx::smem_u32(ahead + (kIn * i + 1) * NT + tid), residual + row * a.K8 + c);
     }
-  }
+  };
+  if (kAhead) copy(blockIdx.x);
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
     const int64_t base = row * a.K8;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
     uint4 vx[V], vr[V];
+    if (kAhead) asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * NT + tid;
-      vx[i] = c < a.K8 ? reinterpret_cast<const uint4*>(a.x)[base + c] : make_uint4(0, 0, 0, 0);
-      if (kRes) vr[i] = c < a.K8 ? reinterpret_cast<const uint4*>(a.residual)[base + c] : make_uint4(0, 0, 0, 0);
+      vx[i] = c >= a.K8 ? zero : kAhead ? ahead[kIn * i * NT + tid] : x[base + c];
+      if (kRes) vr[i] = c >= a.K8 ? zero : kAhead ? ahead[(kIn * i + 1) * NT + tid] : residual[base + c];
     }
-    float h[V][8], sum = 0.f;
-    uint32_t mx = 0;
+    if (kAhead) copy(row + gridDim.x);
+    float h[V][8], sum = 0.f, most = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      const int c = i * NT + tid;
       unpack8(vx[i], h[i]);
       if (kRes) {
         float r[8];
         unpack8(vr[i], r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] += r[j];
-        const int c = i * NT + tid;
         if (c < a.K8) reinterpret_cast<uint4*>(a.h)[base + c] = pack8(h[i]);
       }
       float wf[8];
-      if (kFp8) unpack8(w[i], wf);
+      if (kFp8) unpack8(c < a.K8 ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : zero, wf);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         sum = fmaf(h[i][j], h[i][j], sum);
         if (kFp8) {
           h[i][j] *= wf[j];
-          mx = max(mx, mag(h[i][j]));
+          most = fmaxf(most, fabsf(h[i][j]));
         }
       }
     }
+    uint32_t mx = __float_as_uint(most);  // order as their bits; a NaN is in the sum
     block_reduce<true, kFp8>(sum, mx, red, parity);
     const float f = norm_factor<kFp8>(a, row, sum, mx);
 #pragma unroll
@@ -400,14 +417,37 @@ unsigned row_ctas(int64_t M, int threads) {
   return (unsigned)(M < fit ? M : fit);
 }
 
+// Allows a kernel more than 48 KB of dynamic shared memory, once per device;
+// `set` has one bit per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& set) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return cudaErrorInvalidDevice;
+  if (set.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) set.fetch_or(uint64_t(1) << dev, std::memory_order_acq_rel);
+  return e;
+}
+
+template <int V, bool kRes, bool kFp8, bool kWide>
+cudaError_t launch_norm_v(const NormArgs& a, int threads, cudaStream_t stream) {
+  auto kernel = rmsnorm_kernel<V, kRes, kFp8, kWide>;
+  if (V < 4) return launch_rows(kernel, a, row_ctas(a.M, threads), threads, stream);
+  static std::atomic<uint64_t> set{0};
+  constexpr size_t kRowBytes = (size_t)V * (kRes ? 2 : 1) * 16;  // per thread
+  cudaError_t e = allow_smem(kernel, kRowBytes * 1024, set);
+  return e != cudaSuccess ? e : launch_rows(kernel, a, row_ctas(a.M, threads), threads, stream, kRowBytes * threads);
+}
+
 template <bool kRes, bool kFp8>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
   if (a.K8 > 4096) return launch_rows(rmsnorm_long_kernel<kRes, kFp8>, a, row_ctas(a.M, 1024), 1024, stream);
   const int V = row_vectors(a.K8, kFp8);
   const int t = row_threads(a.K8, V);
-  if (V == 1) return launch_rows(rmsnorm_kernel<1, kRes, kFp8>, a, row_ctas(a.M, t), t, stream);
-  if (V == 2) return launch_rows(rmsnorm_kernel<2, kRes, kFp8>, a, row_ctas(a.M, t), t, stream);
-  return launch_rows(rmsnorm_kernel<4, kRes, kFp8>, a, row_ctas(a.M, t), t, stream);
+  if (V == 4) return launch_norm_v<4, kRes, kFp8, true>(a, t, stream);
+  if (V == 2)
+    return t > 512 ? launch_norm_v<2, kRes, kFp8, true>(a, t, stream) : launch_norm_v<2, kRes, kFp8, false>(a, t, stream);
+  return t > 512 ? launch_norm_v<1, kRes, kFp8, true>(a, t, stream) : launch_norm_v<1, kRes, kFp8, false>(a, t, stream);
 }
 
 }  // namespace
@@ -428,14 +468,9 @@ cudaError_t launch_silu_mul(const __half* gate_up, __half* y, uint8_t* x8, float
     const int t = row_threads(a.F8, V);
     if (V == 1) return launch_rows(silu_mul_fp8_kernel<1>, a, row_ctas(M, t), t, stream);
     if (V == 2) return launch_rows(silu_mul_fp8_kernel<2>, a, row_ctas(M, t), t, stream);
-    static std::atomic<uint64_t> attr_set{0};  // one bit per device that has the attribute
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return cudaErrorInvalidDevice;
-    if (!(attr_set.load(std::memory_order_acquire) >> dev & 1)) {
-      cudaError_t e = cudaFuncSetAttribute(silu_mul_fp8_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * 32 * 1024);
-      if (e != cudaSuccess) return e;
-      attr_set.fetch_or(uint64_t(1) << dev, std::memory_order_acq_rel);
-    }
+    static std::atomic<uint64_t> set{0};
+    cudaError_t e = allow_smem(silu_mul_fp8_kernel<4>, (size_t)4 * 32 * 1024, set);
+    if (e != cudaSuccess) return e;
     return launch_rows(silu_mul_fp8_kernel<4>, a, row_ctas(M, t), t, stream, (size_t)4 * 32 * t);
   }
   constexpr int V = 2;
