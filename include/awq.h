@@ -259,7 +259,8 @@ awq_status awq_w4a8_gemm(const void* x8, const void* sx, const void* qweight, co
  * With residual fp16 [M][K], h = x + residual, and h rounded to fp16 is
  * written to h fp16 [M][K] (the next residual; y is made from the sum before
  * that rounding). h may be the same buffer as x or residual. Without a
- * residual (NULL), h = x and the argument h must be NULL too. eps >= 0.
+ * residual (NULL), h = x and the argument h must be NULL too. eps >= 0; with
+ * eps = 0 a row of zeros gives NaN (0 / 0), as the formula does.
  * Source: none on the pages (the norm ahead of the linear layers). */
 awq_status awq_rmsnorm(const void* x, const void* residual, const void* weight, float eps, void* h, void* y,
                        int64_t M, int64_t K, void* stream);
@@ -287,7 +288,9 @@ awq_status awq_silu_mul_fp8(const void* gate_up, void* x8, void* sx, int64_t M, 
  * 128), each with every kv head (head_dim 64 or 128):
  *   k, v          uint8 [blocks][heads][block_tokens][head_dim], E4M3 codes
  *   k_exp, v_exp  int8  [blocks][heads]
- *   value = code * 2^exp, one exponent per block and head
+ *   value = code * 2^exp, one exponent per block and head (awq_kv8_append
+ *   writes -32 .. 8; awq_kv8_attention takes one below -32 as -32 and one above
+ *   31 as 31)
  * A batch is `seqs` sequences. Sequence b owns rows starts[b] .. starts[b+1]-1
  * of q, k, v and y (its new tokens; there may be none), has lens[b] tokens in
  * all, the new ones being the last, and keeps token j in block
@@ -351,7 +354,7 @@ awq_status awq_kv8_append(const void* k, int64_t k_stride, const void* v, int64_
  * [rows][q_heads * head_dim]; query head i reads kv head i / (q_heads /
  * heads). The row at position p gives
  *   y = sum_{j <= p} softmax_j(scale * q . k_j) v_j,
- * and zeros when it sees no key. Made for the generation stage: one or a few
+ * and zeros when it sees no key (NaN when q is not finite). Made for the generation stage: one or a few
  * new tokens per sequence. More are right too, but every 16 rows of a kv head
  * read the sequence's keys anew. fp32 sums, the softmax weights rounded to
  * fp16 for their product with v. Work is split along the keys as well; parts

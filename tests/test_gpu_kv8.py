@@ -301,6 +301,33 @@ def test_nan_reaches_the_rows_that_see_it():
     assert torch.isnan(y[0, 1]).all() and torch.isfinite(y[0, 0]).all() and torch.isfinite(y[1]).all()
 
 
+@pytest.mark.parametrize("n", [3, 40, 4000])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_queries_give_nan_in_their_own_row(n, sign):
+    # with codes of one sign all scores of the row are +inf or all -inf: 0 / 0 either way
+    bt = Batch([2], [n], 8, 2, 64, 32, seed=16)
+    bt.cache.k.copy_(torch.where((bt.cache.k & 0x7F) == 0, torch.full_like(bt.cache.k, 0x38), bt.cache.k & 0x7F))
+    bt.q = bt.q.clone()
+    bt.q[1, 5, 0] = sign * math.inf
+    y = bt.attend()
+    ref, tol = bt.attention_ref()
+    row = torch.zeros_like(y, dtype=torch.bool)
+    row[1, 5 * 64:6 * 64] = True
+    assert torch.isnan(y[row]).all()
+    assert ((y.double() - ref).abs() <= tol)[~row].all()
+
+
+def test_exponents_of_any_caller():
+    # all 256 values of the exponents: those outside -32 .. 31 count as the nearest of them
+    bt = Batch([1, 2], [128 * 16, 128 * 16], 4, 2, 64, 16, seed=17)
+    bt.cache.v_exp.copy_(torch.arange(bt.cache.v_exp.numel(), device="cuda").view_as(bt.cache.v_exp).to(torch.int8))
+    bt.cache.k_exp.copy_(bt.cache.v_exp.flatten().flip(0).view_as(bt.cache.k_exp))
+    y = bt.attend(scale=2.0 ** -40).clone()
+    for t in (bt.cache.k_exp, bt.cache.v_exp):
+        t.clamp_(-32, 31)
+    assert torch.equal(bt.attend(scale=2.0 ** -40), y) and not torch.isnan(y).any()
+
+
 def test_rows_of_no_sequence_are_left_alone():
     bt = Batch([1, 2], [30, 40], 4, 2, 64, 32, seed=13)
     want = bt.attend()

@@ -326,7 +326,7 @@ constexpr float kNoM = -1e30f;  // M of a row that has seen no key: far below an
 
 // The group of units that starts in a CTA's range and ends in a later one's.
 struct Kv8Fix {
-  int valid, row0, rows, tile0, head, last_cta, pad0, pad1;
+  int valid, row0, rows, tile0, head, last_cta, past, pad;
 };
 
 struct AttnArgs {
@@ -529,6 +529,9 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     key00 = sg.tile0 * kUnitKeys + warp * kStepKeys;
     steps = sg.seen > key00 ? min((sg.seen - key00 + kUnitKeys - 1) / kUnitKeys, sg.n) : 0;
   };
+  // Exponents as they are used: with a spread of 63 no weight that counts leaves
+  // fp32, and 2^e is a number. (The append writes -32 .. 8.)
+  auto usable = [](int e) { return max(min(e, 31), -32); };
   // Blocks and exponents of the next 32 subtiles, one per lane.
   int blk = -1;
   int k_exp = 0, v_exp = 0, k_exp_prev = 0, v_exp_prev = 0;
@@ -617,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
       const int key0 = key00 + step * kUnitKeys;
       // the issuing side is up to kStages - 1 steps ahead: it may have loaded the next 32 already
       const bool same = (step * kSub) / 32 == min(step + L::kStages - 1, steps - 1) * kSub / 32;
-      const float k_of = a.scale_log2 * __int_as_float(((same ? k_exp : k_exp_prev) + 127) << 23);
-      const float v_of = (float)(same ? v_exp : v_exp_prev);
+      const float k_of = a.scale_log2 * __int_as_float((usable(same ? k_exp : k_exp_prev) + 127) << 23);
+      const float v_of = (float)usable(same ? v_exp : v_exp_prev);
 
       // The weights' exponents x + e_v - M of the step's keys (masked keys: -inf)
       float x[kSub][NT][4], unit[kSub];  // unit: 2^-e_v
@@ -813,8 +816,10 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
         den = fmaf(f, v.y, den);
       }
       if (w.starts && w.ends) {
-        const float inv = den == 0.f ? 0.f : 1.f / den;  // a row that sees no key is zero
-        const int64_t at = (int64_t)(w.row0 + (w.r0 + r) / a.group) * cache.heads * a.group + (int64_t)w.head * a.group + (w.r0 + r) % a.group;
+        const int token = (w.r0 + r) / a.group;
+        // a row that sees no key is zero; one whose scores are all -infinity is 0 / 0
+        const float inv = min(w.past + token + 1, w.len) > 0 ? 1.f / den : 0.f;
+        const int64_t at = (int64_t)(w.row0 + token) * cache.heads * a.group + (int64_t)w.head * a.group + (w.r0 + r) % a.group;
         *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(f2h(sum.x * inv, sum.y * inv), f2h(sum.z * inv, sum.w * inv));
       } else {
         *reinterpret_cast<float4*>(slot + r * D + d) = sum;
@@ -822,12 +827,17 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
       }
     }
     if (w.starts && !w.ends && tid == 0)  // the CTA that holds the group's last unit: the last c with first_unit(c) < its end
-      a.fix[blockIdx.x] = Kv8Fix{1, w.row0, w.rows, w.r0, w.head, (int)min((w.end * ctas + total - 1) / total, ctas) - 1, 0, 0};
+      a.fix[blockIdx.x] = Kv8Fix{1, w.row0, w.rows, w.r0, w.head, (int)min((w.end * ctas + total - 1) / total, ctas) - 1, w.past, 0};
     ptx::fence_proxy_async_smem();  // copies will come where the parts were
     hand_out(turn);
     if (__syncthreads_or(dead)) break;
   }
-  // After a timeout, copies still on their way must land before this CTA is gone.
+  // After a timeout, copies still on their way must land before this CTA is gone:
+  // first those of the step whose wait gave up, which `stage` has left behind.
+  if (dead) {
+    const bool wrapped = stage == 0;
+    ptx::drain_bar(bars + 8 * (wrapped ? L::kStages - 1 : stage - 1), parity ^ (wrapped ? 1u : 0u));
+  }
   for (; stage != fill; stage = stage == L::kStages - 1 ? 0 : stage + 1, parity ^= stage == 0)
     ptx::drain_bar(bars + 8 * stage, parity);
 }
@@ -894,8 +904,9 @@ __global__ void __launch_bounds__(kThreads) kv8_fixup_kernel(const AttnArgs a, i
       }
     }
   }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  const int64_t at = (int64_t)(f.row0 + (f.tile0 + r) / a.group) * heads * a.group + (int64_t)f.head * a.group + (f.tile0 + r) % a.group;
+  const int token = (f.tile0 + r) / a.group;
+  const float inv = f.past + token + 1 > 0 ? 1.f / den : 0.f;  // as in the attention kernel (such groups have keys)
+  const int64_t at = (int64_t)(f.row0 + token) * heads * a.group + (int64_t)f.head * a.group + (f.tile0 + r) % a.group;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<uint32_t*>(a.out + at * D + 32 * e + 2 * lane) = f2h(sum[e] * inv, sum[e + 1] * inv);
