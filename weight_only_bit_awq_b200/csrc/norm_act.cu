@@ -299,7 +299,7 @@ __device__ __forceinline__ float silu_factor(const SiluArgs& a, int64_t row, uin
 // a thread there is one CTA on an SM, so nothing would be loaded while it
 // computes: there the next row's inputs are copied to shared memory meanwhile,
 // by the threads that will use them, so that needs no barrier (2048 x 28672:
-// 51.9 against 55.4 us; with two CTAs, at 14336, it changed nothing).
+// 46.8 against 55.4 us; with two CTAs, at 14336, it changed nothing).
 template <int V>
 __global__ void __launch_bounds__(1024) silu_mul_fp8_kernel(const SiluArgs a) {
   constexpr bool kAhead = V == 4;
@@ -411,7 +411,11 @@ cudaError_t launch_rows(void (*kernel)(Args), const Args& a, unsigned ctas, int 
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// CTAs that walk M rows: as many as fit the SMs at once (2048 threads each).
+// CTAs that walk M rows: as many as fit the SMs at once by 2048 threads each. The
+// two kernels with four vectors a thread fit one: the SiLU gets that many
+// (2048 x 28672: 46.8 against 49.6 us, 4000 x 18944 64.2 against 67.3), the norm,
+// for which a second set of shorter walks is as good or better, as many as others
+// (2000 x 20480 to fp16 55.3 against 58.7, 2048 x 28672 to E4M3 65.9 against 66.4).
 unsigned row_ctas(int64_t M, int threads) {
   const int64_t fit = (int64_t)device_info().sm_count * (2048 / threads);
   return (unsigned)(M < fit ? M : fit);
@@ -471,7 +475,8 @@ cudaError_t launch_silu_mul(const __half* gate_up, __half* y, uint8_t* x8, float
     static std::atomic<uint64_t> set{0};
     cudaError_t e = allow_smem(silu_mul_fp8_kernel<4>, (size_t)4 * 32 * 1024, set);
     if (e != cudaSuccess) return e;
-    return launch_rows(silu_mul_fp8_kernel<4>, a, row_ctas(M, t), t, stream, (size_t)4 * 32 * t);
+    // registers leave room for one CTA on an SM
+    return launch_rows(silu_mul_fp8_kernel<4>, a, row_ctas(M, 2048), t, stream, (size_t)4 * 32 * t);
   }
   constexpr int V = 2;
   const int parts = (a.F8 + 256 * V - 1) / (256 * V);
