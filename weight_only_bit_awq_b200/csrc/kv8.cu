@@ -338,7 +338,6 @@ struct AttnArgs {
   float* partial;     // [ctas][2][slot]
   int slot;           // floats of a slot: rows * (D + 2)
   Kv8Fix* fix;        // [ctas]
-  int cache_rows;     // blocks * heads * block_tokens
   bool whole;         // groups are not split between CTAs
 };
 
@@ -352,6 +351,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
+}
+// 16 bytes from global to shared memory; zeros for bytes = 0.
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 // Four 8 x 16-byte pieces: lane i gives the address of token i % 8 of piece i / 8.
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -381,7 +384,7 @@ struct Attn {
   static constexpr int kPartBytes = kStepKeys * D;            // a warp's step of K, or of V
   static constexpr int kStageBytes = 2 * kPartBytes;
   static_assert(kStageBytes >= kRows * D * 4, "a warp's part of the output fits a stage");
-  static constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;  // room to align
+  static constexpr int kSmem = kWarps * kStages * kStageBytes + 128;  // room to align
   static constexpr int kSlot = kRows * (D + 2);
   static constexpr int kCtasPerSm = kStages * kStageBytes <= 16384 ? 3 : 2;  // by shared memory and registers
 };
@@ -396,30 +399,18 @@ struct Segment {
 
 template <int D, int NT, int ST>
 __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
-    kv8_attention_kernel(const AttnArgs a, const Kv8Cache cache, const Kv8Batch bt,
-                         const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                         uint32_t* status) {
+    kv8_attention_kernel(const AttnArgs a, const Kv8Cache cache, const Kv8Batch bt, uint32_t* status) {
   using L = Attn<D, NT, ST>;
   constexpr int KS = D / 16;     // k-steps of S
   constexpr int MT = D / 16;     // channel tiles of O
   extern __shared__ char smem_raw[];
-  char* const smem = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);  // the swizzle goes by address
+  char* const smem = smem_raw + (-ptx::smem_u32(smem_raw) & 127u);  // the pieces' places are computed by XOR
   __shared__ int64_t scan[kWarps];
   __shared__ Place place;
-  __shared__ __align__(8) uint64_t full[kWarps * L::kStages];
-  __shared__ uint32_t abort_word;
   __shared__ float2 ml[kWarps][L::kRows];  // M and l of the warps' rows
   __shared__ const float* parts[kWarps];
   __shared__ Segment ahead[2];
   __shared__ int ahead_valid[2];
-  volatile uint32_t* const abort_flag = &abort_word;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kWarps * L::kStages; ++i) ptx::mbar_init(ptx::smem_u32(&full[i]), 1);
-    abort_word = 0;
-    ptx::fence_mbarrier_init();
-    ptx::prefetch_tensormap(&kmap);
-    ptx::prefetch_tensormap(&vmap);
-  }
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
@@ -446,13 +437,15 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   Place p = find_item(bt.seqs, items, before, u, &place);
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * (L::kStages * L::kStageBytes);
-  const uint32_t bars = ptx::smem_u32(&full[warp * L::kStages]);
   // The lane's row and piece of an ldmatrix: tokens (lane & 15), the first of
   // two neighbouring pieces for lanes below 16; pieces are swizzled by token.
   const uint32_t lrow = lane & 15, swz = D == 128 ? (lane & 7) : (lane >> 1 & 3);
   const uint32_t lane_off = lrow * D + (((lane >> 4) ^ swz) << 4);
   int stage = 0, fill = 0;   // ring positions of the next step to use and to fill
-  uint32_t parity = 0;
+  // The lane's piece of 512 contiguous bytes of codes (512 / D tokens), and its
+  // place: pieces are swizzled by token.
+  const uint32_t put_row = lane / (D / 16), put_swz = D == 128 ? put_row : (put_row >> 1 & 3);
+  const uint32_t put = put_row * D + ((lane % (D / 16) ^ put_swz) << 4);
 
   // ---- segments: the parts of groups in this CTA's range. The first warp walks
   // the batch one segment ahead and hands them out, so that all warps take the
@@ -553,31 +546,30 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
       }
     }
   };
-  // The boxes of a step's K and V: 32 tokens each, or two of 16 where that is
-  // the block. A box of a block that is not there starts behind the cache's last
-  // row, which reads as zeros. Issuing takes the elected lane about 190 cycles a
-  // box: a quarter of a step. (A warp of its own for it falls behind on small
-  // blocks, and four of them leave the others too few registers.)
-  const bool two = bs == 16;
+  // A step's K and V: 512 contiguous bytes an instruction, 16 tokens of a block
+  // after the other. A block that is not there, or that no row sees, is zeros.
+  // One group of copies per call, so that a step is the oldest of kStages.
   auto issue = [&](int step) {
-    if (step >= steps) return;
-    if ((step * kSub) % 32 == 0) load_info(step * kSub);
-    const uint32_t bar = bars + 8 * fill, dst = ring + fill * L::kStageBytes;
-    fill = fill == L::kStages - 1 ? 0 : fill + 1;
-    const int key = key00 + step * kUnitKeys;
-    const int id0 = __shfl_sync(0xffffffffu, blk, step * kSub), id1 = __shfl_sync(0xffffffffu, blk, step * kSub + 1);
-    const int row0 = id0 < 0 ? a.cache_rows : (id0 * cache.heads + sg.head) * bs + (key & (bs - 1));
-    const int row1 = id1 < 0 ? a.cache_rows : (id1 * cache.heads + sg.head) * bs;
-    __syncwarp();  // every lane has read what the stage held
-    if (ptx::elect_one()) {
-      ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
-      ptx::tma_load_2d(dst, &kmap, 0, row0, bar);
-      ptx::tma_load_2d(dst + L::kPartBytes, &vmap, 0, row0, bar);
-      if (two) {
-        ptx::tma_load_2d(dst + 16 * D, &kmap, 0, row1, bar);
-        ptx::tma_load_2d(dst + L::kPartBytes + 16 * D, &vmap, 0, row1, bar);
+    if (step < steps) {
+      if ((step * kSub) % 32 == 0) load_info(step * kSub);
+      const uint32_t dst = ring + fill * L::kStageBytes + put;
+      fill = fill == L::kStages - 1 ? 0 : fill + 1;
+      const int key = key00 + step * kUnitKeys;
+      __syncwarp();  // every lane has read what the stage held
+#pragma unroll
+      for (int sb = 0; sb < kSub; ++sb) {
+        const int id = __shfl_sync(0xffffffffu, blk, step * kSub + sb);
+        const uint32_t bytes = id < 0 ? 0 : 16;
+        const int64_t at = ((int64_t)(max(id, 0) * cache.heads + sg.head) * bs + ((key + 16 * sb) & (bs - 1))) * D + 16 * lane;
+#pragma unroll
+        for (int i = 0; i < 16 * D / 512; ++i) {
+          const uint32_t to = (dst + sb * (16 * D) + i * 512) ^ (D == 128 ? (i & 1) << 6 : 0);
+          copy16(to, cache.k + at + i * 512, bytes);
+          copy16(to + L::kPartBytes, cache.v + at + i * 512, bytes);
+        }
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto begin_segment = [&]() {  // its first steps and its q on their way
     begin_steps();
@@ -586,7 +578,6 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     load_q();
   };
 
-  bool dead = false;  // a wait gave up: no more copies, the results are garbage
   hand_out(0);
   __syncthreads();
   bool have = ahead_valid[0];
@@ -611,12 +602,12 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    for (int step = 0; step < steps && !dead; ++step) {
+    for (int step = 0; step < steps; ++step) {
       issue(step + L::kStages - 1);
-      dead = !__all_sync(0xffffffffu, ptx::wait_bar(bars + 8 * stage, parity, abort_flag, status));
+      asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 1) : "memory");
+      __syncwarp();  // the other lanes' copies are there too
       const uint32_t src = ring + stage * L::kStageBytes + lane_off;
       stage = stage == L::kStages - 1 ? 0 : stage + 1;
-      parity ^= stage == 0;
       const int key0 = key00 + step * kUnitKeys;
       // the issuing side is up to kStages - 1 steps ahead: it may have loaded the next 32 already
       const bool same = (step * kSub) / 32 == min(step + L::kStages - 1, steps - 1) * kSub / 32;
@@ -775,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     first = false;
     have = ahead_valid[turn ^ 1];
     sg = ahead[turn ^ 1];
-    if (have && !dead) begin_segment();
+    if (have) begin_segment();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -828,18 +819,9 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     }
     if (w.starts && !w.ends && tid == 0)  // the CTA that holds the group's last unit: the last c with first_unit(c) < its end
       a.fix[blockIdx.x] = Kv8Fix{1, w.row0, w.rows, w.r0, w.head, (int)min((w.end * ctas + total - 1) / total, ctas) - 1, w.past, 0};
-    ptx::fence_proxy_async_smem();  // copies will come where the parts were
     hand_out(turn);
-    if (__syncthreads_or(dead)) break;
+    __syncthreads();  // copies will come where the parts were
   }
-  // After a timeout, copies still on their way must land before this CTA is gone:
-  // first those of the step whose wait gave up, which `stage` has left behind.
-  if (dead) {
-    const bool wrapped = stage == 0;
-    ptx::drain_bar(bars + 8 * (wrapped ? L::kStages - 1 : stage - 1), parity ^ (wrapped ? 1u : 0u));
-  }
-  for (; stage != fill; stage = stage == L::kStages - 1 ? 0 : stage + 1, parity ^= stage == 0)
-    ptx::drain_bar(bars + 8 * stage, parity);
 }
 
 // Adds the parts of the groups that more than one CTA worked on, in a fixed
@@ -942,22 +924,9 @@ cudaError_t launch_attention(AttnArgs a, const Kv8Cache& cache, const Kv8Batch& 
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(uint64_t(1) << dev, std::memory_order_acq_rel);
   }
-  CUtensorMap maps[2];
-  for (int i = 0; i < 2; ++i) {
-    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)a.cache_rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)D};
-    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)(bt.block_tokens < kStepKeys ? bt.block_tokens : kStepKeys)};
-    const cuuint32_t estr[2] = {1, 1};
-    auto encode = tensor_map_encoder();
-    if (!encode) return cudaErrorNotSupported;
-    if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, i ? cache.v : cache.k, dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
   a.slot = L::kSlot;
   const int ctas = L::kCtasPerSm * device_info().sm_count;  // all resident: a persistent grid
-  cudaError_t e = launch_pdl(kv8_attention_kernel<D, NT, ST>, dim3((unsigned)ctas), kThreads, L::kSmem, stream, a, cache, bt, maps[0], maps[1], status);
+  cudaError_t e = launch_pdl(kv8_attention_kernel<D, NT, ST>, dim3((unsigned)ctas), kThreads, L::kSmem, stream, a, cache, bt, status);
   if (e != cudaSuccess || a.whole) return e;
   // groups of units at most; with eight or more parts each, a CTA per row
   const int64_t groups = (int64_t)cache.heads * (bt.seqs + (int64_t)bt.rows * a.group / L::kRows);
@@ -1002,7 +971,6 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
   a.out = out;
   a.group = q_heads / cache.heads;
   a.scale_log2 = scale * kLog2e;
-  a.cache_rows = (int)(cache.blocks * cache.heads * bt.block_tokens);
   // ("not many": about as many groups as sequences and tokens times kv heads)
   a.whole = (int64_t)bt.table_width * bt.block_tokens <= kWholeKeys &&
             ((int64_t)bt.seqs + bt.rows) * cache.heads <= 8 * device_info().sm_count;
