@@ -394,7 +394,15 @@ struct Segment {
   int b, row0, len, past, rows, r0, head, tile0, n;
   int seen;     // keys that some row sees
   bool starts, ends;
-  int64_t end;  // of the group, in units
+  int left;     // units of the group behind it
+};
+
+// Where a CTA is in its range.
+struct Walk {
+  int64_t todo;  // units left
+  Seq s;
+  int b, head, tile, tiles;  // the sequence, and the group in it: kv head, row tile of `tiles`
+  int v0, per;   // the next unit of the group, its units
 };
 
 template <int D, int NT, int ST>
@@ -406,35 +414,38 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   extern __shared__ char smem_raw[];
   char* const smem = smem_raw + (-ptx::smem_u32(smem_raw) & 127u);  // the pieces' places are computed by XOR
   __shared__ int64_t scan[kWarps];
-  __shared__ Place place;
+  __shared__ Walk walk;
   __shared__ float2 ml[kWarps][L::kRows];  // M and l of the warps' rows
   __shared__ const float* parts[kWarps];
-  __shared__ Segment ahead[2];
-  __shared__ int ahead_valid[2];
+  __shared__ Segment ahead[3];
+  __shared__ int ahead_valid[3];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int bs = bt.block_tokens, shift = __ffs(bs) - 1;
-  auto row_tiles = [&](const Seq& s) { return ((int64_t)s.tokens * a.group + L::kRows - 1) / L::kRows; };
+  auto row_tiles = [&](const Seq& s) { return (int)(((int64_t)s.tokens * a.group + L::kRows - 1) / L::kRows); };
   // a sequence with no keys still has one (empty) unit per row tile: its rows are zero
   auto key_tiles = [&](const Seq& s) { return max((s.len + kUnitKeys - 1) / kUnitKeys, 1); };
   // what a group of the sequence counts in the split
   auto group_units = [&](const Seq& s) { return a.whole ? 1 : key_tiles(s) + kGroupCost; };
   auto items = [&](int b) -> int64_t {
     const Seq s = load_seq(bt, b, status);
-    return row_tiles(s) * group_units(s) * cache.heads;
+    return (int64_t)row_tiles(s) * group_units(s) * cache.heads;
   };
-  if (threadIdx.x == 0) place = Place{0, 0};
+  if (tid == 0) walk.todo = ahead_valid[0] = 0;
   int64_t before;
   const int64_t total = total_items(bt.seqs, items, scan, before);
   const int64_t ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
   if (tid == 0) a.fix[blockIdx.x].valid = 0;
   if ((int64_t)blockIdx.x >= ctas) return;
-  auto first_unit = [&](int64_t c) { return total / ctas * c + total % ctas * c / ctas; };
-  int64_t u = first_unit(blockIdx.x);
-  const int64_t u1 = first_unit((int64_t)blockIdx.x + 1);
-  Place p = find_item(bt.seqs, items, before, u, &place);
+  // a 64-bit division takes as long as a step
+  const bool small = total * gridDim.x <= 0x7FFFFFFF;
+  auto divide = [&](int64_t x, int64_t y) -> int64_t { return small ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y; };
+  auto first_unit = [&](int64_t c) {
+    return small ? divide(total * c, ctas) : total / ctas * c + total % ctas * c / ctas;
+  };
+  const int64_t u = first_unit(blockIdx.x), u1 = first_unit((int64_t)blockIdx.x + 1);
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * (L::kStages * L::kStageBytes);
   // The lane's row and piece of an ldmatrix: tokens (lane & 15), the first of
@@ -447,57 +458,79 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   const uint32_t put_row = lane / (D / 16), put_swz = D == 128 ? put_row : (put_row >> 1 & 3);
   const uint32_t put = put_row * D + ((lane % (D / 16) ^ put_swz) << 4);
 
-  // ---- segments: the parts of groups in this CTA's range. The first warp walks
-  // the batch one segment ahead and hands them out, so that all warps take the
-  // same steps even if the lists change under them.
+  // ---- segments: the parts of groups in this CTA's range. One thread walks the
+  // batch two segments ahead and hands them out, so that all warps take the same
+  // steps even if the lists change under them.
   Segment sg;
-  const bool small = total <= 0x7FFFFFFF;
-  auto divide = [&](int64_t x, int64_t y) -> int64_t {  // a 64-bit division takes as long as a step
-    return small ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
-  };
-  auto next_segment = [&](Segment& sg) -> bool {
-    while (u < u1) {
-      Seq s = load_seq(bt, p.b, status);
-      int64_t n_seq = row_tiles(s) * group_units(s) * cache.heads;
-      while (u >= p.base + n_seq) {
-        if (p.b + 1 >= bt.seqs) return false;
-        p.base += n_seq;
-        s = load_seq(bt, ++p.b, status);
-        n_seq = row_tiles(s) * group_units(s) * cache.heads;
-      }
-      const int per = group_units(s);
-      const int64_t in_seq = u - p.base, group_no = divide(in_seq, per);
-      const int v0 = (int)(in_seq - group_no * per);
-      const int take = (int)(u1 - u < per - v0 ? u1 - u : per - v0);
-      sg.tile0 = max(v0 - kGroupCost, 0);
-      sg.n = a.whole ? key_tiles(s) : v0 + take - kGroupCost - sg.tile0;
-      u += take;
-      if (sg.n <= 0) continue;  // only of the units that stand for the group's fixed cost
-      sg.head = (int)divide(group_no, row_tiles(s));
-      sg.r0 = (int)(group_no - (int64_t)sg.head * row_tiles(s)) * L::kRows;
-      sg.b = p.b;
-      sg.row0 = s.row0;
-      sg.len = s.len;
-      sg.past = s.len - s.tokens;
-      sg.rows = s.tokens * a.group;
-      sg.seen = max(min(sg.past + (min(sg.r0 + L::kRows, sg.rows) - 1) / a.group + 1, s.len), 0);
-      sg.starts = sg.tile0 == 0;
-      sg.ends = v0 + take == per;
-      sg.end = p.base + (group_no + 1) * per;
-      return true;
-    }
-    return false;
-  };
-
   auto hand_out = [&](int slot) {
-    if (warp != 0) return;
-    Segment s;
-    const bool more = next_segment(s);
-    if (lane == 0) {
+    Walk w = walk;
+    bool found = false;
+    while (w.todo > 0) {
+      if (w.v0 == w.per) {  // the next group
+        w.v0 = 0;
+        if (++w.tile >= w.tiles) {
+          w.tile = 0;
+          if (++w.head >= cache.heads) {
+            w.head = 0;
+            w.tiles = 0;
+            while (w.tiles == 0 && ++w.b < bt.seqs) {
+              w.s = load_seq(bt, w.b, status);
+              w.tiles = row_tiles(w.s);
+            }
+            if (w.tiles == 0) break;
+            w.per = group_units(w.s);
+          }
+        }
+      }
+      const int take = (int)(w.todo < w.per - w.v0 ? w.todo : w.per - w.v0);
+      Segment s;
+      s.tile0 = max(w.v0 - kGroupCost, 0);
+      s.n = a.whole ? key_tiles(w.s) : w.v0 + take - kGroupCost - s.tile0;
+      w.v0 += take;
+      w.todo -= take;
+      if (s.n <= 0) continue;  // only of the units that stand for the group's fixed cost
+      s.head = w.head;
+      s.r0 = w.tile * L::kRows;
+      s.b = w.b;
+      s.row0 = w.s.row0;
+      s.len = w.s.len;
+      s.past = w.s.len - w.s.tokens;
+      s.rows = w.s.tokens * a.group;
+      s.seen = max(min(s.past + (min(s.r0 + L::kRows, s.rows) - 1) / a.group + 1, s.len), 0);
+      s.starts = s.tile0 == 0;
+      s.ends = w.v0 == w.per;
+      s.left = w.per - w.v0;
       ahead[slot] = s;
-      ahead_valid[slot] = more;
+      found = true;
+      break;
     }
+    walk = w;
+    ahead_valid[slot] = found;
   };
+  {  // the thread that counted the sequence of the first unit begins
+    const int per = (bt.seqs + kThreads - 1) / kThreads;
+    int64_t at = before;
+    for (int b = tid * per; b < min(bt.seqs, (tid + 1) * per); ++b) {
+      const Seq s = load_seq(bt, b, status);
+      const int tiles = row_tiles(s), units = group_units(s);
+      const int64_t n = (int64_t)tiles * units * cache.heads;
+      if (u >= at && u < at + n) {
+        const int64_t group_no = divide(u - at, units);
+        Walk w;
+        w.todo = u1 - u;
+        w.s = s;
+        w.b = b;
+        w.head = (int)divide(group_no, tiles);
+        w.tile = (int)(group_no - (int64_t)w.head * tiles);
+        w.tiles = tiles;
+        w.v0 = (int)(u - at - group_no * units);
+        w.per = units;
+        walk = w;
+        hand_out(0);
+      }
+      at += n;
+    }
+  }
 
   // ---- a segment's query rows as B fragments, channels in K's order
   uint32_t qf[NT][KS][2];
@@ -578,14 +611,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     load_q();
   };
 
-  hand_out(0);
   __syncthreads();
   bool have = ahead_valid[0];
   sg = ahead[0];
   if (have) begin_segment();
-  hand_out(1);
+  if (tid == 0) hand_out(1), hand_out(2);
+  __syncwarp();
   bool first = true;
-  for (int turn = 0; have; turn ^= 1) {
+  for (int turn = 0, next = 1; have; turn = next, next = next == 2 ? 0 : next + 1) {
     int limit[NT][2];  // keys that the lane's two rows of each column tile see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -761,11 +794,11 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     }
 
     // ---- the next segment's copies start before this one's parts are merged
-    const Segment w = sg;
-    if (first) __syncthreads();  // the second segment is there (later ones: a merge's barrier)
+    const Segment& w = ahead[turn];
+    if (first) __syncthreads();  // the second segment is there (later ones: the last merge's barrier)
     first = false;
-    have = ahead_valid[turn ^ 1];
-    sg = ahead[turn ^ 1];
+    have = ahead_valid[next];
+    sg = ahead[next];
     if (have) begin_segment();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -818,9 +851,10 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
       }
     }
     if (w.starts && !w.ends && tid == 0)  // the CTA that holds the group's last unit: the last c with first_unit(c) < its end
-      a.fix[blockIdx.x] = Kv8Fix{1, w.row0, w.rows, w.r0, w.head, (int)min((w.end * ctas + total - 1) / total, ctas) - 1, w.past, 0};
-    hand_out(turn);
+      a.fix[blockIdx.x] = Kv8Fix{1, w.row0, w.rows, w.r0, w.head, (int)min(((u1 + w.left) * ctas + total - 1) / total, ctas) - 1, w.past, 0};
     __syncthreads();  // copies will come where the parts were
+    if (tid == 0) hand_out(turn);
+    __syncwarp();
   }
 }
 
