@@ -1024,8 +1024,8 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
     return few ? launch_attention<128, 1, 3>(a, cache, bt, status, stream)
                : launch_attention<128, 1, 2>(a, cache, bt, status, stream);
   }
-  return rows <= 8 ? launch_attention<64, 1, 3>(a, cache, bt, status, stream)
-                   : launch_attention<64, 2, 3>(a, cache, bt, status, stream);
+  return rows <= 8 ? launch_attention<64, 1, 2>(a, cache, bt, status, stream)
+                   : launch_attention<64, 2, 2>(a, cache, bt, status, stream);
 }
 
 }  // namespace awq
