@@ -291,10 +291,12 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
 // sums fp32.
 //
 // Bound by HBM: every code is read once, 4 flops a code and row. Each warp has
-// a ring of its own in shared memory, filled by TMA boxes of whole tokens that
-// it asks for itself; warps never wait for one another within a segment, and
-// the next segment's first copies start before a segment's parts are merged.
-// The boxes are swizzled by 16-byte pieces, so that ldmatrix, which takes one
+// a ring of its own in shared memory that its lanes fill with 16-byte copies, 512
+// contiguous bytes an instruction; warps never wait for one another within a
+// segment, and the next segment's first copies start before a segment's parts
+// are merged. (Tiled copies by one lane took it 190 cycles a box, a quarter of a
+// step: 1 x 131002 tokens 53.1 against 51.9 us, 48 x 64 wide 43.2 against 41.4.)
+// The 16-byte pieces are swizzled by token, so that ldmatrix, which takes one
 // piece of 8 tokens at a time, has no bank conflicts. As 16-bit elements those
 // pieces are pairs of codes: for K, lane (g, t) gets channels 4t .. 4t + 3 of
 // token g, the A fragment of one k-step (the k order is free as long as q
@@ -313,14 +315,14 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
 constexpr float kPOffset = 12.f, kPMost = 15.f;
 // A group costs about as much as this many units more: its q, its first copies'
 // latency, the merge of the warps' parts. CTAs get equal ranges of units with
-// these counted (48 ragged sequences: 85 us without, 72 us with two).
+// these counted (48 ragged sequences: 78.5 us without, 72.2 with two; with 64-wide
+// heads 51.4 and 40.0; three change them by less than 1 %).
 constexpr int kGroupCost = 2;
 // Where the block table holds no more keys than this, and the groups are not
-// many times the CTAs, a CTA takes whole groups and there is no fixup kernel:
-// one sequence of 128 / 512 / 1024 tokens 5.7 /
-// 8.4 / 12.1 us against 7.6 / 8.2 / 8.7 us split, 32 sequences of 256 to 512
-// tokens 8.0 to 8.8 against 10.6 to 11.6 us, and a launch less to wait for (but
-// 256 sequences of 20 to 400: 38.8 against 36.5 us).
+// many times the CTAs, a CTA takes whole groups and there is no fixup kernel: one
+// sequence of 128 / 512 / 1024 tokens 5.4 / 8.2 / 11.8 us against 7.0 / 7.6 / 7.9
+// split, 32 sequences of 256 to 512 tokens 10.8 against 12.7 us, and a launch less
+// to wait for (but 256 sequences of 20 to 400: 37.5 against 34.9 us).
 constexpr int kWholeKeys = 512;
 constexpr float kNoM = -1e30f;  // M of a row that has seen no key: far below any x, finite
 
@@ -1015,9 +1017,9 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
   const int64_t rows = ((int64_t)bt.rows + bt.seqs - 1) / bt.seqs * a.group;
   // Few groups (long sequences) keep one stream per warp: a ring of three steps
   // and two CTAs per SM. Many groups want more of them under way: two steps
-  // and three CTAs. One sequence of 131002 tokens: 52.8 against 54.5 us; 256
-  // of 20 to 400: 45.4 against 38.4; 16 of 500 to 2047 with 32 kv heads: 39.3
-  // against 36.4. (Several row tiles and 64-wide heads: no such difference.)
+  // and three CTAs. One sequence of 131002 tokens: 51.4 against 53.1 us; 256
+  // of 20 to 400: 40.5 against 35.2. (Several row tiles have no room for three;
+  // 64-wide heads do as well with two steps.)
   const bool few = ((int64_t)bt.seqs + bt.rows) * cache.heads * 8 <= 2 * device_info().sm_count;
   if (cache.head_dim == 128) {
     if (rows > 8) return launch_attention<128, 2, 3>(a, cache, bt, status, stream);
