@@ -301,6 +301,21 @@ def test_nan_reaches_the_rows_that_see_it():
     assert torch.isnan(y[0, 1]).all() and torch.isfinite(y[0, 0]).all() and torch.isfinite(y[1]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(5, 4), (3, 8), (4, 1)])   # two row tiles of 16, or one of 8
+def test_nan_codes_of_v_at_every_place(T, G, D):
+    for n in range(33, 50):
+        bt = Batch([T], [n], 2 * G, 2, D, 32, seed=n)
+        token, channel, head = n - 1 - n % T, (7 * n) % D, n % 2
+        want = bt.attend().view(T, 2 * G, D).clone()
+        bt.cache.v[int(bt.table[0, token // 32]), head, token % 32, channel] = 0xFF if n % 3 else 0x7F
+        y = bt.attend().view(T, 2 * G, D)
+        hit = torch.zeros_like(y, dtype=torch.bool)
+        hit[T - n + token:, head * G:(head + 1) * G, channel] = True
+        assert torch.equal(torch.isnan(y), hit), (n, token, channel)
+        assert torch.equal(y[~hit], want[~hit])
+
+
 @pytest.mark.parametrize("n", [3, 40, 4000])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_infinite_queries_give_nan_in_their_own_row(n, sign):

@@ -413,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   using L = Attn<D, NT, ST>;
   constexpr int KS = D / 16;     // k-steps of S
   constexpr int MT = D / 16;     // channel tiles of O
+  constexpr bool kWide = NT == 2;
   extern __shared__ char smem_raw[];
   char* const smem = smem_raw + (-ptx::smem_u32(smem_raw) & 127u);  // the pieces' places are computed by XOR
   __shared__ int64_t scan[kWarps];
@@ -557,6 +558,13 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     key00 = sg.tile0 * kUnitKeys + warp * kStepKeys;
     steps = sg.seen > key00 ? min((sg.seen - key00 + kUnitKeys - 1) / kUnitKeys, sg.n) : 0;
   };
+  // Which of the lane's two rows element c of an S or O fragment belongs to, their
+  // numbers in the tile, the lanes of a row, and the key of an S element in a subtile.
+  auto row_of = [](int c) { return kWide ? c >> 1 : c & 1; };
+  auto lane_row = [&](int c) { return kWide ? g + 8 * c : 2 * t + c; };
+  auto key_of = [&](int nt, int c) { return kWide ? 8 * nt + 2 * t + (c & 1) : g + 8 * (c >> 1); };
+  constexpr int kRowLane = kWide ? 1 : 4, kRowLanes = kWide ? 4 : 8;
+
   // Exponents as they are used: with a spread of 63 no weight that counts leaves
   // fp32, and 2^e is a number. (The append writes -32 .. 8.)
   auto usable = [](int e) { return max(min(e, 31), -32); };
@@ -621,21 +629,18 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   __syncwarp();
   bool first = true;
   for (int turn = 0, next = 1; have; turn = next, next = next == 2 ? 0 : next + 1) {
-    int limit[NT][2];  // keys that the lane's two rows of each column tile see
+    int limit[2];  // keys that the lane's two rows see
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) limit[nt][c] = min(sg.past + (sg.r0 + 8 * nt + 2 * t + c) / a.group + 1, sg.len);
+    for (int c = 0; c < 2; ++c) limit[c] = min(sg.past + (sg.r0 + lane_row(c)) / a.group + 1, sg.len);
     const int least = sg.past + sg.r0 / a.group + 1;  // keys that every row sees
 
-    float o[NT][MT][4], M[NT][2], l[NT][2];
+    float o[MT][NT][4], M[2], l[2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      M[nt][0] = M[nt][1] = steps > 0 ? 0.f : kNoM;  // 0 until the first step sets it
-      l[nt][0] = l[nt][1] = 0.f;
-    }
+      for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+    M[0] = M[1] = steps > 0 ? 0.f : kNoM;  // 0 until the first step sets it
+    l[0] = l[1] = 0.f;
 
     for (int step = 0; step < steps; ++step) {
       issue(step + L::kStages - 1);
@@ -663,9 +668,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
           ldsm4((src + sb * (16 * D)) ^ (ks << 4), w);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t a0 = lo_h2(w[2 * i]), a1 = lo_h2(w[2 * i + 1]), a2 = hi_h2(w[2 * i]), a3 = hi_h2(w[2 * i + 1]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(x[sb][nt], a0, a1, a2, a3, qf[nt][ks + i][0], qf[nt][ks + i][1]);
+            const uint32_t k0 = lo_h2(w[2 * i]), k1 = lo_h2(w[2 * i + 1]), k2 = hi_h2(w[2 * i]), k3 = hi_h2(w[2 * i + 1]);
+            if constexpr (kWide) {
+              const uint32_t(&q0)[2] = qf[0][ks + i], (&q1)[2] = qf[NT - 1][ks + i];
+              mma16816(x[sb][0], q0[0], q1[0], q0[1], q1[1], k0, k2);
+              mma16816(x[sb][NT - 1], q0[0], q1[0], q0[1], q1[1], k1, k3);
+            } else {
+              mma16816(x[sb][0], k0, k1, k2, k3, qf[0][ks + i][0], qf[0][ks + i][1]);
+            }
           }
         }
 #pragma unroll
@@ -676,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[sb][nt][c] = fmaf(x[sb][nt][c], k_unit, ev - M[nt][c & 1]);
+          for (int c = 0; c < 4; ++c) x[sb][nt][c] = fmaf(x[sb][nt][c], k_unit, ev - M[row_of(c)]);
       }
       if (key0 + kStepKeys > least) {  // some row does not see all of the step's keys
 #pragma unroll
@@ -685,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (key0 + 16 * sb + g + 8 * (c >> 1) >= limit[nt][c & 1]) x[sb][nt][c] = -INFINITY;
+              if (key0 + 16 * sb + key_of(nt, c) >= limit[row_of(c)]) x[sb][nt][c] = -INFINITY;
       }
 
       // Where one exceeds kPMost, and in a segment's first step, every row's M
@@ -698,48 +708,57 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
 #pragma unroll
           for (int c = 0; c < 4; ++c) over = fmaxf(over, x[sb][nt][c]);
       if (__any_sync(0xffffffffu, over > kPMost) || step == 0) {
+        float up[2] = {kNoM, kNoM};  // by how much M moves
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float up[2];  // by how much M moves
+        for (int sb = 0; sb < kSub; ++sb)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float m = kNoM;
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int sb = 0; sb < kSub; ++sb) m = fmaxf(m, fmaxf(x[sb][nt][c], x[sb][nt][c + 2]));
+            for (int c = 0; c < 4; ++c) up[row_of(c)] = fmaxf(up[row_of(c)], x[sb][nt][c]);
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-            up[c] = step == 0 ? m - kPOffset : fmaxf(m - kPOffset, 0.f);
-            M[nt][c] += up[c];
-          }
+        for (int r = 0; r < 2; ++r) {
 #pragma unroll
-          for (int sb = 0; sb < kSub; ++sb)
+          for (int w = kRowLane; w < kRowLane * kRowLanes; w <<= 1) up[r] = fmaxf(up[r], __shfl_xor_sync(0xffffffffu, up[r], w));
+          up[r] = step == 0 ? up[r] - kPOffset : fmaxf(up[r] - kPOffset, 0.f);
+          M[r] += up[r];
+        }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) x[sb][nt][c] -= up[c & 1];
-          if (step == 0) continue;  // nothing to rescale yet
+        for (int sb = 0; sb < kSub; ++sb)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[sb][nt][c] -= up[row_of(c)];
+        if (step > 0) {  // in the first step there is nothing to rescale
           const float f[2] = {ex2(-up[0]), ex2(-up[1])};
-          l[nt][0] *= f[0], l[nt][1] *= f[1];
+          l[0] *= f[0], l[1] *= f[1];
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            o[nt][i][0] *= f[0], o[nt][i][1] *= f[1];
-            o[nt][i][2] *= f[0], o[nt][i][3] *= f[1];
-          }
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[i][nt][c] *= f[row_of(c)];
         }
       }
 
-      uint32_t pf[kSub][NT][2];
+      uint32_t pf[kSub][2 * NT];
 #pragma unroll
-      for (int sb = 0; sb < kSub; ++sb)
+      for (int sb = 0; sb < kSub; ++sb) {
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float pr[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) pr[c] = ex2(x[sb][nt][c]);
-          l[nt][0] = fmaf(pr[0] + pr[2], unit[sb], l[nt][0]);
-          l[nt][1] = fmaf(pr[1] + pr[3], unit[sb], l[nt][1]);
-          pf[sb][nt][0] = transpose8x8(f2h(pr[0], pr[1]));
-          pf[sb][nt][1] = transpose8x8(f2h(pr[2], pr[3]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sum[row_of(c)] += pr[c];
+          pf[sb][2 * nt] = f2h(pr[0], pr[1]);
+          pf[sb][2 * nt + 1] = f2h(pr[2], pr[3]);
+          if (!kWide) pf[sb][0] = transpose8x8(pf[sb][0]), pf[sb][1] = transpose8x8(pf[sb][1]);
         }
-      // O += V^T P^T. Where a row does not see all 16 keys of a subtile, a NaN
+        l[0] = fmaf(sum[0], unit[sb], l[0]);
+        l[1] = fmaf(sum[1], unit[sb], l[1]);
+      }
+      // O += P V. Where a row does not see all 16 keys of a subtile, a NaN
       // code must reach only the rows that see it: 0 * NaN in the MMA would
       // reach all. Such codes are taken out there, and their channels of the
       // rows that see them set to NaN. (Places behind the end can hold NaN codes
@@ -764,17 +783,20 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
                 for (int j = 0; j < 4; ++j) {
                   w[j] &= ~((nan[j] >> 7) * 0xFFu);
 #pragma unroll 1
-                  for (int tt = 0; tt < 4; ++tt) {  // the four lanes that share this lane's channels
-                    const uint32_t m = __shfl_sync(0xffffffffu, nan[j], (lane & ~3) | tt);
+                  for (int s = 0; s < 4 * NT; ++s) {  // the lanes that share this lane's channels
+                    const int gg = kWide ? 2 * t + (s >> 2) : g, tt = s & 3;
+                    const uint32_t m = __shfl_sync(0xffffffffu, nan[j], 4 * gg + tt);
                     if (m == 0) continue;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int b = 0; b < 4; ++b)  // byte b: token + (b >> 1), channel + (b & 1)
 #pragma unroll
-                      for (int b = 0; b < 4; ++b)  // byte b: token + (b >> 1), channel + (b & 1)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                          if ((m >> (8 * b + 7) & 1) && key + 2 * tt + 8 * (j & 1) + (b >> 1) < limit[nt][c])
-                            o[nt][i + (j >> 1)][2 * (b & 1) + c] = NAN;
+                      for (int r = 0; r < 2; ++r)
+                        if ((m >> (8 * b + 7) & 1) && key + 2 * tt + 8 * (j & 1) + (b >> 1) < limit[r]) {
+                          float(&to)[NT][4] = o[i + (j >> 1)];
+                          if (!kWide) to[0][2 * (b & 1) + r] = NAN;
+                          else if (s < 4) to[(b & 1) % NT][2 * r] = NAN;
+                          else to[(b & 1) % NT][2 * r + 1] = NAN;
+                        }
                   }
                 }
               }
@@ -782,9 +804,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const uint32_t p0 = __byte_perm(w[2 * j], 0, 0x3120), p1 = __byte_perm(w[2 * j + 1], 0, 0x3120);
-              const uint32_t a0 = lo_h2(p0), a1 = hi_h2(p0), a2 = lo_h2(p1), a3 = hi_h2(p1);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i + j], a0, a1, a2, a3, pf[sb][nt][0], pf[sb][nt][1]);
+              const uint32_t v0 = lo_h2(p0), v1 = hi_h2(p0), v2 = lo_h2(p1), v3 = hi_h2(p1);
+              if constexpr (kWide) {  // channels of even number, then of odd
+                const uint32_t(&p)[2 * NT] = pf[sb];
+                mma16816(o[i + j][0], p[0], p[1], p[2 * NT - 2], p[2 * NT - 1], v0, v2);
+                mma16816(o[i + j][NT - 1], p[0], p[1], p[2 * NT - 2], p[2 * NT - 1], v1, v3);
+              } else {
+                mma16816(o[i + j][0], v0, v1, v2, v3, pf[sb][0], pf[sb][1]);
+              }
             }
           }
         }
@@ -803,24 +830,26 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     sg = ahead[next];
     if (have) begin_segment();
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+      for (int x = kRowLane; x < kRowLane * kRowLanes; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
     // Each warp leaves its part in the stage of its ring that is still free.
-    // Columns are swapped by 16 in every second pair of rows: fewer conflicts.
+    // Columns are swapped by 16 in every second row (wide), or pair of rows: fewer
+    // conflicts.
     float* const mine = reinterpret_cast<float*>(smem + (ring - ptx::smem_u32(smem)) + fill * L::kStageBytes);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int c = 0; c < 2; ++c) {
+      const int r = lane_row(c);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = 8 * nt + 2 * t + c;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-          *reinterpret_cast<float2*>(mine + r * D + ((16 * i + 2 * g) ^ ((t & 1) << 4))) = make_float2(o[nt][i][c], o[nt][i][c + 2]);
-        if (g == 0) ml[warp][r] = make_float2(M[nt][c], l[nt][c]);
+      for (int i = 0; i < MT; ++i) {
+        if constexpr (kWide)
+          *reinterpret_cast<float4*>(mine + r * D + ((16 * i + 4 * t) ^ ((r & 1) << 4))) =
+              make_float4(o[i][0][2 * c], o[i][NT - 1][2 * c], o[i][0][2 * c + 1], o[i][NT - 1][2 * c + 1]);
+        else
+          *reinterpret_cast<float2*>(mine + r * D + ((16 * i + 2 * g) ^ ((t & 1) << 4))) = make_float2(o[i][0][c], o[i][0][c + 2]);
       }
+      if ((kWide ? t : g) == 0) ml[warp][r] = make_float2(M[c], l[c]);
+    }
     if (lane == 0) parts[warp] = mine;
     __syncthreads();
     float* slot = a.partial + ((int64_t)blockIdx.x * 2 + (w.starts ? 1 : 0)) * a.slot;
@@ -836,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
       for (int j = 0; j < kWarps; ++j) {
         const float2 v = ml[j][r];
         const float f = ex2(v.x - mx);
-        const float4 ow = *reinterpret_cast<const float4*>(parts[j] + r * D + (d ^ ((r >> 1 & 1) << 4)));
+        const float4 ow = *reinterpret_cast<const float4*>(parts[j] + r * D + (d ^ ((kWide ? r & 1 : r >> 1 & 1) << 4)));
         sum.x = fmaf(f, ow.x, sum.x), sum.y = fmaf(f, ow.y, sum.y);
         sum.z = fmaf(f, ow.z, sum.z), sum.w = fmaf(f, ow.w, sum.w);
         den = fmaf(f, v.y, den);
