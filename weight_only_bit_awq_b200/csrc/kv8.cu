@@ -283,12 +283,14 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
 // attention
 // ---------------------------------------------------------------------------
 
-// S^T = K q^T and O^T = V^T P^T with mma.sync m16n8k16: the keys (of S) and
-// the head's channels (of O) are the MMA's 16 rows, the query rows its 8
-// columns, so the few rows of a generation step (query heads that share a kv
-// head, times new tokens) waste half as much as they would as the 16-row
-// operand. Codes become exact fp16 in registers; the products are exact, the
-// sums fp32.
+// mma.sync m16n8k16, in two forms. Up to 8 query rows (query heads that share a kv
+// head, times new tokens): S^T = K q^T and O^T = V^T P^T, the keys (of S) and the
+// head's channels (of O) are the instruction's 16 rows, the query rows its 8
+// columns, so few rows waste half as much; the weights are transposed on the way.
+// More rows (kWide): S = q K^T and O = P V, 16 query rows are its rows, and the
+// weights come out of S as the next operand (drafts of 1 to 5 tokens, 64 wide 25.1
+// us against 26.1 as two column tiles of 8). Codes become exact fp16 in registers;
+// the products are exact, the sums fp32.
 //
 // Bound by HBM: every code is read once, 4 flops a code and row. Each warp has
 // a ring of its own in shared memory that its lanes fill with 16-byte copies, 512
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
 // The 16-byte pieces are swizzled by token, so that ldmatrix, which takes one
 // piece of 8 tokens at a time, has no bank conflicts. As 16-bit elements those
 // pieces are pairs of codes: for K, lane (g, t) gets channels 4t .. 4t + 3 of
-// token g, the A fragment of one k-step (the k order is free as long as q
+// token g, the fragment of one k-step (the k order is free as long as q
 // follows it); for V, transposed, it gets channels 2g and 2g + 1 of tokens 2t
 // and 2t + 1, and one byte permutation makes them fragments.
 //
@@ -378,7 +380,7 @@ constexpr int kSub = 2;
 constexpr int kStepKeys = 16 * kSub;
 constexpr int kUnitKeys = kWarps * kStepKeys;
 
-// D: head dimension; NT: column tiles of 8 query rows; ST: steps in a warp's ring.
+// D: head dimension; NT: query rows of a tile, in eights (1 or 2); ST: steps in a warp's ring.
 template <int D, int NT, int ST>
 struct Attn {
   static constexpr int kRows = 8 * NT;
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     }
   }
 
-  // ---- a segment's query rows as B fragments, channels in K's order
+  // ---- a segment's query rows as fragments, channels in K's order
   uint32_t qf[NT][KS][2];
   auto load_q = [&]() {
 #pragma unroll
@@ -1046,12 +1048,16 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
   const int64_t rows = ((int64_t)bt.rows + bt.seqs - 1) / bt.seqs * a.group;
   // Few groups (long sequences) keep one stream per warp: a ring of three steps
   // and two CTAs per SM. Many groups want more of them under way: two steps
-  // and three CTAs. One sequence of 131002 tokens: 51.4 against 53.1 us; 256
-  // of 20 to 400: 40.5 against 35.2. (Several row tiles have no room for three;
-  // 64-wide heads do as well with two steps.)
-  const bool few = ((int64_t)bt.seqs + bt.rows) * cache.heads * 8 <= 2 * device_info().sm_count;
+  // and three CTAs. One sequence of 131002 tokens: 51.4 against 53.1 us, with four
+  // new tokens 53.5 against 58.5; 256 of 20 to 400: 40.5 against 35.2, 48 of 30 to
+  // 8000 with two new tokens of 64 query heads 77.7 against 73.6. (64-wide heads do
+  // as well with two steps.)
+  const int64_t groups = (int64_t)cache.heads * (bt.seqs + (int64_t)bt.rows * a.group / (rows > 8 ? 16 : 8));  // at most
+  const bool few = groups * 8 <= 2 * device_info().sm_count;
   if (cache.head_dim == 128) {
-    if (rows > 8) return launch_attention<128, 2, 3>(a, cache, bt, status, stream);
+    if (rows > 8)
+      return few ? launch_attention<128, 2, 3>(a, cache, bt, status, stream)
+                 : launch_attention<128, 2, 2>(a, cache, bt, status, stream);
     return few ? launch_attention<128, 1, 3>(a, cache, bt, status, stream)
                : launch_attention<128, 1, 2>(a, cache, bt, status, stream);
   }
