@@ -154,7 +154,7 @@ __device__ __forceinline__ int needed_exponent(uint32_t mag) {
 
 // One CTA per (block that gets new tokens, kv head), for K and V. The block's
 // new rows stay in registers between the maximum and the conversion, so they
-// are read once, and their loads start before the block number is known.
+// are read once, and their loads do not wait for the block number.
 // Bound by HBM for prompts (2 bytes read, 1 written an element), by the launch
 // and four dependent loads for single tokens. Heads are the grid's fastest
 // dimension: the CTAs that run together read whole rows of k and v.
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
   const int r0 = threadIdx.x / pieces, c = threadIdx.x % pieces;
   const int64_t row0 = (int64_t)s.row0 + (int64_t)j * bs - past;  // source row of the block's token 0
 
+  const int blk = bt.table[(int64_t)p.b * bt.table_width + j];
   uint4 x[2][kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
@@ -201,7 +202,6 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
       x[1][i] = *reinterpret_cast<const uint4*>(vnew + (row0 + r) * v_stride + at);
     }
   }
-  const int blk = bt.table[(int64_t)p.b * bt.table_width + j];
   if (blk < 0 || blk >= cache.blocks) {
     if (threadIdx.x == 0) record_status(status, AWQ_ERR_BOUNDS);
     return;
