@@ -424,6 +424,36 @@ def test_attention_is_deterministic_and_replays_in_a_graph():
     assert bt.status() == awq.AWQ_OK
 
 
+def test_two_streams_at_once():
+    # two batches over one cache, each with its own workspace, on two streams
+    one = Batch([1] * 20, [300 + 90 * i for i in range(20)], 32, 8, 128, 64, seed=23)
+    other = Batch([3] * 20, one.n, 32, 8, 128, 64, seed=24)
+    other.cache, other.table = one.cache, one.table
+    torch.cuda.synchronize()
+    want = [b.attend().clone() for b in (one, other)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, b in enumerate((one, other)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(b.attend())
+    torch.cuda.synchronize()
+    for i, b in enumerate((one, other)):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+        assert b.status() == awq.AWQ_OK
+
+
+@pytest.mark.parametrize("T", [4, 5, 9])
+@pytest.mark.parametrize("D,block", [(128, 64), (64, 16)])
+def test_few_long_sequences_with_drafts(T, D, block):
+    # 16-row tiles (4 to 9 tokens of 4 query heads), both depths of the ring
+    for lens in ([20011], [9000, 77, 4100, 12345, 3, 8191]):
+        bt = Batch([T] * len(lens), lens, 32, 8, D, block, seed=25)
+        bt.append()
+        bt.check((T, lens))
+
+
 def test_strided_rows_and_binding_checks():
     bt = Batch([1, 1, 1], [40, 50, 60], 8, 2, 64, 32, seed=16)
     want = bt.attend()
