@@ -253,7 +253,7 @@ awq_status awq_w4a8_gemm(const void* x8, const void* sx, const void* qweight, co
  * K, F <= 2^22, M <= 2^24, M * F <= 2^40 (else AWQ_ERR_UNSUPPORTED). Every
  * pointer is 16-byte aligned. Outputs may not overlap inputs or one another
  * (AWQ_ERR_INVALID_ARG), but for h below. A row that holds an infinity or a
- * NaN gives a y, or an sx, that is not finite. */
+ * NaN, or meets one in the weights, gives a y, or an sx, that is not finite. */
 
 /* y = h * rsqrt(mean_k h^2 + eps) * weight, y fp16 [M][K], weight fp16 [K].
  * With residual fp16 [M][K], h = x + residual, and h rounded to fp16 is

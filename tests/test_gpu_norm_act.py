@@ -247,3 +247,21 @@ def test_offsets_beyond_32_bits():
     check_fp16(awq.awq_silu_mul(x)[tail], silu_ref(x[tail]), rel, "silu")
     x8, sx = awq.awq_silu_mul_fp8(x)
     check_fp8(x8[tail], sx[tail], silu_ref(x[tail]), rel, "silu fp8")
+
+
+@pytest.mark.parametrize("K", [264, 4096, 8192, 20480, 33000])
+@pytest.mark.parametrize("with_residual", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_rmsnorm_of_weights_that_are_not_finite(K, with_residual, bad):
+    # the formula's y is not finite at that channel (0 * infinity is NaN too), so no row has a finite scale
+    x, r, w = inputs(3, K, seed=5)
+    x[1], r[1] = 0, 0
+    r = r if with_residual else None
+    for where in (slice(K // 2, K // 2 + 1), slice(0, K)):
+        wb = w.clone()
+        wb[where] = bad
+        y = awq.awq_rmsnorm(x, wb, EPS, residual=r)
+        y = y[0] if with_residual else y
+        assert not torch.isfinite(y[:, where]).any(), where
+        sx = awq.awq_rmsnorm_fp8(x, wb, EPS, residual=r)[1]
+        assert not torch.isfinite(sx).any(), where

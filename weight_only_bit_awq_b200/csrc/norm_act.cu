@@ -65,6 +65,13 @@ __device__ __forceinline__ float rcp(float x) {
 // every number, so the maximum also tells a row that is not finite.
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// Maximum that is NaN when an operand is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Sum of `s` (kSum) and maximum of `m` (kMax) over the CTA; `red` holds two
 // buffers that alternate from row to row, so one barrier a row is enough.
 template <bool kSum, bool kMax>
@@ -99,7 +106,8 @@ struct NormArgs {
 
 // The row factor of y (fp16 output) or of the codes (E4M3 output, where the
 // row's scale is stored too); m: largest |h w|. A row with an infinity or a NaN
-// has a sum that is not finite: its y, or its sx, is not finite either.
+// has a sum that is not finite, under a weight that is one m is not: then y, or
+// sx, is not finite either.
 template <bool kFp8>
 __device__ __forceinline__ float norm_factor(const NormArgs& a, int64_t row, float sum, uint32_t m) {
   const float rs = rsqrtf(sum * a.inv_k + a.eps), mx = __uint_as_float(m);
@@ -171,11 +179,11 @@ __global__ void __launch_bounds__(kWide ? 1024 : 512, V <= 2 ? 2 : 1) rmsnorm_ke
         sum = fmaf(h[i][j], h[i][j], sum);
         if (kFp8) {
           h[i][j] *= wf[j];
-          most = fmaxf(most, fabsf(h[i][j]));
+          most = max_nan(most, fabsf(h[i][j]));
         }
       }
     }
-    uint32_t mx = __float_as_uint(most);  // order as their bits; a NaN is in the sum
+    uint32_t mx = __float_as_uint(most);  // order as their bits, a NaN (of x, the residual or the weights) above all
     block_reduce<true, kFp8>(sum, mx, red, parity);
     const float f = norm_factor<kFp8>(a, row, sum, mx);
 #pragma unroll
