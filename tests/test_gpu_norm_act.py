@@ -265,3 +265,37 @@ def test_rmsnorm_of_weights_that_are_not_finite(K, with_residual, bad):
         assert not torch.isfinite(y[:, where]).any(), where
         sx = awq.awq_rmsnorm_fp8(x, wb, EPS, residual=r)[1]
         assert not torch.isfinite(sx).any(), where
+
+
+# rows beyond 16384 copy the next row ahead while they work: enough rows that
+# every CTA walks several
+@pytest.mark.parametrize("K", [16392, 20480, 28672, 32768])
+@pytest.mark.parametrize("form", ["plain", "residual", "onto x", "onto residual"])
+def test_wide_rmsnorm_walks_rows(K, form):
+    M = 700
+    x, r, w = inputs(M, K, seed=6)
+    ref = norm_ref(x, w, EPS, None if form == "plain" else r)
+    if form == "plain":
+        check_fp16(awq.awq_rmsnorm(x, w, EPS), ref, fp32_slack(K), (form, K))
+        check_fp8(*awq.awq_rmsnorm_fp8(x, w, EPS), ref, fp32_slack(K), (form, K))
+        return
+    want = (x.float() + r.float()).half()
+    for fp8 in (False, True):
+        xi, ri = x.clone(), r.clone()
+        h = {"residual": None, "onto x": xi, "onto residual": ri}[form]
+        if fp8:
+            x8, sx, h = awq.awq_rmsnorm_fp8(xi, w, EPS, residual=ri, h=h)
+            check_fp8(x8, sx, ref, fp32_slack(K), (form, K))
+        else:
+            y, h = awq.awq_rmsnorm(xi, w, EPS, residual=ri, h=h)
+            check_fp16(y, ref, fp32_slack(K), (form, K))
+        assert torch.equal(h, want)
+
+
+@pytest.mark.parametrize("F", [16392, 20480, 28672, 32768])
+def test_wide_silu_mul_walks_rows(F):
+    g = torch.Generator(device="cuda").manual_seed(F)
+    gu = (torch.randn(700, 2 * F, generator=g, device="cuda") * 2).half()
+    rel = (float(gu[:, :F].abs().max()) + 16) * 2.0 ** -23
+    check_fp8(*awq.awq_silu_mul_fp8(gu), silu_ref(gu), rel, F)
+    check_fp16(awq.awq_silu_mul(gu), silu_ref(gu), rel, F)
