@@ -288,9 +288,9 @@ awq_status awq_silu_mul_fp8(const void* gate_up, void* x8, void* sx, int64_t M, 
  * 128), each with every kv head (head_dim 64 or 128):
  *   k, v          uint8 [blocks][heads][block_tokens][head_dim], E4M3 codes
  *   k_exp, v_exp  int8  [blocks][heads]
- *   value = code * 2^exp, one exponent per block and head (awq_kv8_append
- *   writes -32 .. 8; awq_kv8_attention takes one below -32 as -32 and one above
- *   31 as 31)
+ *   value = code * 2^exp, one exponent per block and head (what awq_kv8_append
+ *   needs is -32 .. 8; of a caller's own, both calls take one below -32 as -32 and
+ *   one above 31 as 31)
  * A batch is `seqs` sequences. Sequence b owns rows starts[b] .. starts[b+1]-1
  * of q, k, v and y (its new tokens; there may be none), has lens[b] tokens in
  * all, the new ones being the last, and keeps token j in block

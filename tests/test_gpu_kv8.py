@@ -560,3 +560,18 @@ def test_both_ways_of_sharing_out_the_work(capacity):
     table[:, :bt.table.shape[1]] = bt.table
     bt.table = table
     bt.check(capacity)
+
+
+def test_append_beside_exponents_of_any_caller():
+    # blocks that hold tokens under each of the 256 exponents, as the attention
+    # reads them (-32 .. 31), get a token more: what they held keeps its value
+    for seed, std in ((26, 1.0), (27, 2e-7), (28, 2e4)):
+        bt = Batch([1] * 256, [6 + b % 9 for b in range(256)], 4, 2, 64, 16, seed=seed, spare=0)
+        bt.k, bt.v = bt.k * std, bt.v * std
+        e = torch.arange(-128, 128, device="cuda").to(torch.int8)
+        bt.cache.k_exp[bt.table[:, 0].long()] = e[:, None].expand(-1, 2)
+        bt.cache.v_exp[bt.table[:, 0].long()] = e.flip(0)[:, None].expand(-1, 2)
+        want = append_model(bt, [bt.cache.k, bt.cache.v, bt.cache.k_exp.clamp(-32, 31), bt.cache.v_exp.clamp(-32, 31)])
+        bt.append()
+        same_cache(bt.cache, want)
+        assert bt.status() == awq.AWQ_OK

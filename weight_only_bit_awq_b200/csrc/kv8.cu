@@ -148,6 +148,11 @@ __device__ __forceinline__ int needed_exponent(uint32_t mag) {
   return (int)(f >> 23) - 127 - 8 + ((f & 0x7FFFFFu) > 0x600000u);
 }
 
+// Exponents as both calls use them, whatever a caller's cache holds: with a spread
+// of 63 no weight that counts leaves fp32, and 2^e is a number. (The append's own
+// are -32 .. 8.)
+__device__ __forceinline__ int usable(int e) { return max(min(e, 31), -32); }
+
 // ---------------------------------------------------------------------------
 // append
 // ---------------------------------------------------------------------------
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
   bool odd[2];  // this thread has an infinity or a NaN
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
-    e_old[part] = lo > 0 ? (int)*exps[part] : -128;
+    e_old[part] = lo > 0 ? usable(*exps[part]) : -128;
     uint32_t m2 = 0;  // two maxima of fp16 magnitudes
 #pragma unroll
     for (int i = 0; i < kIter; ++i) m2 = __vmaxu2(m2, max_mag(x[part][i]));
@@ -567,9 +572,6 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
   auto key_of = [&](int nt, int c) { return kWide ? 8 * nt + 2 * t + (c & 1) : g + 8 * (c >> 1); };
   constexpr int kRowLane = kWide ? 1 : 4, kRowLanes = kWide ? 4 : 8;
 
-  // Exponents as they are used: with a spread of 63 no weight that counts leaves
-  // fp32, and 2^e is a number. (The append writes -32 .. 8.)
-  auto usable = [](int e) { return max(min(e, 31), -32); };
   // Blocks and exponents of the next 32 subtiles, one per lane.
   int blk = -1;
   int k_exp = 0, v_exp = 0, k_exp_prev = 0, v_exp_prev = 0;
