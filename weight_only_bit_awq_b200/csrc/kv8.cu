@@ -213,11 +213,11 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
   }
   const int64_t at = (int64_t)blk * cache.heads + h;
   int8_t* const exps[2] = {cache.k_exp + at, cache.v_exp + at};
-  int e_old[2];
+  int e_there[2];  // not used before the barrier: its load may take that long
   bool odd[2];  // this thread has an infinity or a NaN
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
-    e_old[part] = lo > 0 ? usable(*exps[part]) : -128;
+    e_there[part] = lo > 0 ? (int)*exps[part] : -128;
     uint32_t m2 = 0;  // two maxima of fp16 magnitudes
 #pragma unroll
     for (int i = 0; i < kIter; ++i) m2 = __vmaxu2(m2, max_mag(x[part][i]));
@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
     uint32_t mag = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mag = max(mag, wmax[part][w]);
-    const int e = max(needed_exponent(mag), e_old[part]);
+    const int e_old = lo > 0 ? usable(e_there[part]) : -128;
+    const int e = max(needed_exponent(mag), e_old);
     if (threadIdx.x == 0) *exps[part] = (int8_t)e;
     uint8_t* dst = (part ? cache.v : cache.k) + at * bs * D + 8 * c;
     const float inv = ldexpf(1.f, -e);
@@ -271,8 +272,8 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
         *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
       }
     }
-    if (e > e_old[part] && lo > 0) {  // the codes that were there, under the larger exponent
-      const float down = ldexpf(1.f, e_old[part] - e);
+    if (e > e_old && lo > 0) {  // the codes that were there, under the larger exponent
+      const float down = ldexpf(1.f, e_old - e);
       for (int r = r0; r < lo; r += rows_per_pass) {
         uint2* old = reinterpret_cast<uint2*>(dst + r * D);
         const uint2 v = *old;
