@@ -575,3 +575,55 @@ def test_append_beside_exponents_of_any_caller():
         bt.append()
         same_cache(bt.cache, want)
         assert bt.status() == awq.AWQ_OK
+
+
+@pytest.mark.parametrize("D,block", [(128, 64), (64, 16), (128, 16), (64, 64), (128, 128)])
+def test_append_of_many_sequences_is_bit_exact(D, block):
+    # more blocks than CTAs: each takes a range of them, over empty sequences too
+    g = torch.Generator().manual_seed(29)
+    new = torch.tensor([0, 1, 1, 3, 40, 130])[torch.randint(0, 6, (1100,), generator=g)]
+    new[100:290] = 0                                 # more than a few times 32 without new tokens
+    new[-40:] = 0
+    past = torch.randint(0, 90, (1100,), generator=g)
+    past[300:320] = -2                               # rows without a place
+    lens = (new + past).clamp(min=0)
+    bt = Batch(new.tolist(), lens.tolist(), 4, 2, D, block, seed=block)
+    want = append_model(bt, bt.cache)
+    keep = [t.clone() for t in bt.cache]
+    bt.append()
+    same_cache(bt.cache, want)
+    assert bt.status() == awq.AWQ_OK
+    # a bad block number in the middle of a CTA's range changes nothing else
+    b = 500 + int((new[500:] > 0).int().argmax())
+    j = int(lens[b] - 1) // block
+    good = int(bt.table[b, j])
+    bt.table[b, j] = bt.blocks
+    for t, x in zip(bt.cache, keep):
+        t.copy_(x)
+    bt.append()
+    assert bt.status() == awq.AWQ_ERR_BOUNDS
+    for w, x in zip(want, keep):
+        w[good] = x[good].cpu()
+    same_cache(bt.cache, want)
+
+
+def test_append_grows_with_the_sequences_and_not_their_square():
+    times = []
+    for B in (4096, 32768):
+        H, D, block = 8, 64, 16
+        cache = awq.new_kv8_cache(B, H, block, D, "cuda")
+        k, v = (torch.randn(B, H, D, device="cuda").half() for _ in "kv")
+        starts = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+        lens = torch.full((B,), 9, dtype=torch.int32, device="cuda")
+        table = torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1)
+        ws = awq.new_kv8_workspace(B, B, H, H, D, "cuda")
+        best = math.inf
+        for _ in range(5):
+            t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            t0.record()
+            awq.awq_kv8_append(k, v, cache, starts, lens, table, ws)
+            t1.record()
+            torch.cuda.synchronize()
+            best = min(best, t0.elapsed_time(t1))
+        times.append(best)
+    assert times[1] < 24 * times[0], times           # 8 times the sequences: 8, where the square would be 64

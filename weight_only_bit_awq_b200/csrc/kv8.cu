@@ -161,9 +161,20 @@ __device__ __forceinline__ int usable(int e) { return max(min(e, 31), -32); }
 // new rows stay in registers between the maximum and the conversion, so they
 // are read once, and their loads do not wait for the block number.
 // Bound by HBM for prompts (2 bytes read, 1 written an element), by the launch
-// and four dependent loads for single tokens. Heads are the grid's fastest
+// and four dependent loads for a few hundred single tokens. Heads are the grid's fastest
 // dimension: the CTAs that run together read whole rows of k and v.
-template <int kIter>  // 16-byte pieces of a block's rows per thread: block_tokens * D / 1024
+//
+// Every CTA reads the batch's lists to find its block. With many sequences that is
+// most of the work and grows with their square, so there (kMany) as many CTAs as
+// about fit at once take equal ranges of blocks, find the first and count on from
+// it. Single tokens, 8 kv heads 128 wide, blocks of 64: 4096 sequences 2919 us with
+// a CTA a block and 202 so, 2048 399 and 89, 512 26.4 and 22.0, but 256 12.5 and
+// 13.1 (blocks of 16, 32 heads: 1024 206 and 100, 512 58.8 and 52.0, 256 25.2 and
+// 27.8). Two and eight CTAs an SM: 4096 sequences 270 and 245 us.
+constexpr int kManySeqs = 1024;
+constexpr int kManyCtasPerSm = 4;
+
+template <int kIter, bool kMany>  // kIter: 16-byte pieces of a block's rows per thread, block_tokens * D / 1024
 __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __restrict__ knew,
                                                               const __half* __restrict__ vnew, int64_t k_stride,
                                                               int64_t v_stride, Kv8Cache cache, Kv8Batch bt,
@@ -183,103 +194,122 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
   if (threadIdx.x == 0) place = Place{0, 0};
   int64_t before;
   const int64_t total = total_items(bt.seqs, items, scan, before);
-  const int64_t u = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
-  if (u >= total) return;
-  const Place p = find_item(bt.seqs, items, before, u, &place);
-  const Seq s = load_seq(bt, p.b, status);
-  const int past = s.len - s.tokens;  // position of the first new row (rows at negative positions have no place)
-  const int j = min((max(past, 0) >> shift) + (int)(u - p.base), bt.table_width - 1);
-  const int h = blockIdx.x;
-  const int lo = max(max(past, 0) - j * bs, 0), hi = min(s.len - j * bs, bs);  // new rows of the block
-  const int pieces = D / 8, rows_per_pass = kThreads / pieces;
-  const int r0 = threadIdx.x / pieces, c = threadIdx.x % pieces;
-  const int64_t row0 = (int64_t)s.row0 + (int64_t)j * bs - past;  // source row of the block's token 0
-
-  const int blk = bt.table[(int64_t)p.b * bt.table_width + j];
-  uint4 x[2][kIter];
-#pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    const int r = r0 + i * rows_per_pass;
-    const int64_t at = (int64_t)h * D + 8 * c;
-    x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
-    if (r >= lo && r < hi) {
-      x[0][i] = *reinterpret_cast<const uint4*>(knew + (row0 + r) * k_stride + at);
-      x[1][i] = *reinterpret_cast<const uint4*>(vnew + (row0 + r) * v_stride + at);
-    }
-  }
-  if (blk < 0 || blk >= cache.blocks) {
-    if (threadIdx.x == 0) record_status(status, AWQ_ERR_BOUNDS);
-    return;
-  }
-  const int64_t at = (int64_t)blk * cache.heads + h;
-  int8_t* const exps[2] = {cache.k_exp + at, cache.v_exp + at};
-  int e_there[2];  // not used before the barrier: its load may take that long
-  bool odd[2];  // this thread has an infinity or a NaN
-#pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    e_there[part] = lo > 0 ? (int)*exps[part] : -128;
-    uint32_t m2 = 0;  // two maxima of fp16 magnitudes
-#pragma unroll
-    for (int i = 0; i < kIter; ++i) m2 = __vmaxu2(m2, max_mag(x[part][i]));
-    uint32_t mag = max(m2 & 0xFFFFu, m2 >> 16);
-    odd[part] = mag >= 0x7C00u;
-    if (odd[part]) {  // infinities and NaN become NaN codes and set no scale: once more, without them
-      mag = 0;
-      for (int i = 0; i < kIter; ++i) mag = max(mag, max_finite_mag(x[part][i]));
-    }
-    mag = __reduce_max_sync(0xffffffffu, mag);
-    if ((threadIdx.x & 31) == 0) wmax[part][threadIdx.x >> 5] = mag;
-  }
-  __syncthreads();  // the maxima are there, and every thread has read the old exponents
-#pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    uint32_t mag = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mag = max(mag, wmax[part][w]);
-    const int e_old = lo > 0 ? usable(e_there[part]) : -128;
-    const int e = max(needed_exponent(mag), e_old);
-    if (threadIdx.x == 0) *exps[part] = (int8_t)e;
-    uint8_t* dst = (part ? cache.v : cache.k) + at * bs * D + 8 * c;
-    const float inv = ldexpf(1.f, -e);
-    if (!odd[part] && e >= -15 && e <= 14) {
-      // 2^-e is an fp16 number, and a product that fp16 does not hold exactly
-      // lies below 2^-14, where every code is zero
-      const __half2 inv2 = __float2half2_rn(inv);
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int r = r0 + i * rows_per_pass;
-        const uint4& v = x[part][i];
-        if (r >= lo && r < hi)
-          *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(code2_h(v.x, inv2) | (code2_h(v.y, inv2) << 16),
-                                                              code2_h(v.z, inv2) | (code2_h(v.w, inv2) << 16));
-      }
-    } else {
-#pragma unroll 1
-      for (int r = r0; r < hi; r += rows_per_pass) {
-        if (r < lo) continue;
-        const __half* s = (part ? vnew + (row0 + r) * v_stride : knew + (row0 + r) * k_stride) + (int64_t)h * D + 8 * c;
-        const uint4 v = *reinterpret_cast<const uint4*>(s);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float2 f = h2f(w[q]);
-          f.x *= inv, f.y *= inv;                 // exact
-          if (!(fabsf(f.x) < INFINITY)) f.x = NAN;  // the conversion would saturate an infinity
-          if (!(fabsf(f.y) < INFINITY)) f.y = NAN;
-          o[q] = code2(f.x, f.y);
+  const int64_t ctas = (int64_t)gridDim.y * gridDim.z, cta = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+  auto first_item = [&](int64_t c) { return !kMany || total <= ctas ? c : total / ctas * c + total % ctas * c / ctas; };
+  const int64_t u0 = first_item(cta), u1 = kMany ? min(first_item(cta + 1), total) : u0 + 1;
+  if (u0 >= total) return;
+  Place p = find_item(bt.seqs, items, before, u0, &place);
+  // Every thread takes the same steps, whatever it reads in the lists.
+  for (int64_t u = u0; u < u1; ++u) {
+    if (kMany && u > u0) {
+      __syncthreads();  // the last item's maxima have been read
+      if (__shfl_sync(0xffffffffu, u - p.base >= items(p.b), 0)) {  // the next sequence with items, 32 at a time
+        p.base = u;
+        for (bool found = false; !found && p.b < bt.seqs - 1;) {
+          const int b = p.b + 1 + (int)(threadIdx.x & 31);
+          const uint32_t m = __ballot_sync(0xffffffffu, b < bt.seqs && items(b) > 0);
+          found = m != 0;
+          p.b = min(p.b + (found ? __ffs(m) : 32), bt.seqs - 1);
         }
-        *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
       }
     }
-    if (e > e_old && lo > 0) {  // the codes that were there, under the larger exponent
-      const float down = ldexpf(1.f, e_old - e);
-      for (int r = r0; r < lo; r += rows_per_pass) {
-        uint2* old = reinterpret_cast<uint2*>(dst + r * D);
-        const uint2 v = *old;
-        const float2 a = h2f(lo_h2(v.x)), b = h2f(hi_h2(v.x)), d = h2f(lo_h2(v.y)), f = h2f(hi_h2(v.y));
-        *old = make_uint2(code2(a.x * down, a.y * down) | (code2(b.x * down, b.y * down) << 16),
-                          code2(d.x * down, d.y * down) | (code2(f.x * down, f.y * down) << 16));
+    const Seq s = load_seq(bt, p.b, status);
+    const int past = s.len - s.tokens;  // position of the first new row (rows at negative positions have no place)
+    const int j = min((max(past, 0) >> shift) + (int)(u - p.base), bt.table_width - 1);
+    const int h = blockIdx.x;
+    const int lo = max(max(past, 0) - j * bs, 0), hi = min(s.len - j * bs, bs);  // new rows of the block
+    const int pieces = D / 8, rows_per_pass = kThreads / pieces;
+    const int r0 = threadIdx.x / pieces, c = threadIdx.x % pieces;
+    const int64_t row0 = (int64_t)s.row0 + (int64_t)j * bs - past;  // source row of the block's token 0
+
+    const int blk = bt.table[(int64_t)p.b * bt.table_width + j];
+    uint4 x[2][kIter];
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int r = r0 + i * rows_per_pass;
+      const int64_t at = (int64_t)h * D + 8 * c;
+      x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
+      if (r >= lo && r < hi) {
+        x[0][i] = *reinterpret_cast<const uint4*>(knew + (row0 + r) * k_stride + at);
+        x[1][i] = *reinterpret_cast<const uint4*>(vnew + (row0 + r) * v_stride + at);
+      }
+    }
+    const bool there = blk >= 0 && blk < cache.blocks;
+    if (!there) {
+      if (threadIdx.x == 0) record_status(status, AWQ_ERR_BOUNDS);
+      if (!kMany) return;
+    }
+    const int64_t at = there ? (int64_t)blk * cache.heads + h : 0;
+    int8_t* const exps[2] = {cache.k_exp + at, cache.v_exp + at};
+    int e_there[2];  // not used before the barrier: its load may take that long
+    bool odd[2];  // this thread has an infinity or a NaN
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      e_there[part] = lo > 0 && there ? (int)*exps[part] : -128;
+      uint32_t m2 = 0;  // two maxima of fp16 magnitudes
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) m2 = __vmaxu2(m2, max_mag(x[part][i]));
+      uint32_t mag = max(m2 & 0xFFFFu, m2 >> 16);
+      odd[part] = mag >= 0x7C00u;
+      if (odd[part]) {  // infinities and NaN become NaN codes and set no scale: once more, without them
+        mag = 0;
+        for (int i = 0; i < kIter; ++i) mag = max(mag, max_finite_mag(x[part][i]));
+      }
+      mag = __reduce_max_sync(0xffffffffu, mag);
+      if ((threadIdx.x & 31) == 0) wmax[part][threadIdx.x >> 5] = mag;
+    }
+    __syncthreads();  // the maxima are there, and every thread has read the old exponents
+    if (!there) continue;
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      uint32_t mag = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mag = max(mag, wmax[part][w]);
+      const int e_old = lo > 0 ? usable(e_there[part]) : -128;
+      const int e = max(needed_exponent(mag), e_old);
+      if (threadIdx.x == 0) *exps[part] = (int8_t)e;
+      uint8_t* dst = (part ? cache.v : cache.k) + at * bs * D + 8 * c;
+      const float inv = ldexpf(1.f, -e);
+      if (!odd[part] && e >= -15 && e <= 14) {
+        // 2^-e is an fp16 number, and a product that fp16 does not hold exactly
+        // lies below 2^-14, where every code is zero
+        const __half2 inv2 = __float2half2_rn(inv);
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const int r = r0 + i * rows_per_pass;
+          const uint4& v = x[part][i];
+          if (r >= lo && r < hi)
+            *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(code2_h(v.x, inv2) | (code2_h(v.y, inv2) << 16),
+                                                                code2_h(v.z, inv2) | (code2_h(v.w, inv2) << 16));
+        }
+      } else {
+#pragma unroll 1
+        for (int r = r0; r < hi; r += rows_per_pass) {
+          if (r < lo) continue;
+          const __half* s = (part ? vnew + (row0 + r) * v_stride : knew + (row0 + r) * k_stride) + (int64_t)h * D + 8 * c;
+          const uint4 v = *reinterpret_cast<const uint4*>(s);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float2 f = h2f(w[q]);
+            f.x *= inv, f.y *= inv;                 // exact
+            if (!(fabsf(f.x) < INFINITY)) f.x = NAN;  // the conversion would saturate an infinity
+            if (!(fabsf(f.y) < INFINITY)) f.y = NAN;
+            o[q] = code2(f.x, f.y);
+          }
+          *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+        }
+      }
+      if (e > e_old && lo > 0) {  // the codes that were there, under the larger exponent
+        const float down = ldexpf(1.f, e_old - e);
+        for (int r = r0; r < lo; r += rows_per_pass) {
+          uint2* old = reinterpret_cast<uint2*>(dst + r * D);
+          const uint2 v = *old;
+          const float2 a = h2f(lo_h2(v.x)), b = h2f(hi_h2(v.x)), d = h2f(lo_h2(v.y)), f = h2f(hi_h2(v.y));
+          *old = make_uint2(code2(a.x * down, a.y * down) | (code2(b.x * down, b.y * down) << 16),
+                            code2(d.x * down, d.y * down) | (code2(f.x * down, f.y * down) << 16));
+        }
       }
     }
   }
@@ -1019,16 +1049,24 @@ cudaError_t launch_kv8_append(const __half* k, const __half* v, int64_t k_stride
   // per full block of them and two at the ends
   int64_t items = (int64_t)bt.rows / bt.block_tokens + 2 * (int64_t)bt.seqs;
   if (items > bt.rows) items = bt.rows;
+  const int64_t fit = max(kManyCtasPerSm * device_info().sm_count / cache.heads, 1);
+  const bool many = bt.seqs >= kManySeqs && items > fit;
+  if (many) items = fit;
   const unsigned gy = items < 65535 ? (unsigned)items : 65535u;
   const dim3 grid(cache.heads, gy, (unsigned)((items + gy - 1) / gy));
-  switch (bt.block_tokens * cache.head_dim / 1024) {
-    case 1: return launch_pdl(kv8_append_kernel<1>, grid, kThreads, 0, stream, k, v, k_stride, v_stride, cache, bt, status);
-    case 2: return launch_pdl(kv8_append_kernel<2>, grid, kThreads, 0, stream, k, v, k_stride, v_stride, cache, bt, status);
-    case 4: return launch_pdl(kv8_append_kernel<4>, grid, kThreads, 0, stream, k, v, k_stride, v_stride, cache, bt, status);
-    case 8: return launch_pdl(kv8_append_kernel<8>, grid, kThreads, 0, stream, k, v, k_stride, v_stride, cache, bt, status);
-    case 16: return launch_pdl(kv8_append_kernel<16>, grid, kThreads, 0, stream, k, v, k_stride, v_stride, cache, bt, status);
-    default: return cudaErrorInvalidConfiguration;
-  }
+  auto launch = [&](auto many) -> cudaError_t {
+    auto start = [&](auto kernel) { return launch_pdl(kernel, grid, kThreads, 0, stream, k, v, k_stride, v_stride, cache, bt, status); };
+    constexpr bool kMany = decltype(many)::value;
+    switch (bt.block_tokens * cache.head_dim / 1024) {
+      case 1: return start(kv8_append_kernel<1, kMany>);
+      case 2: return start(kv8_append_kernel<2, kMany>);
+      case 4: return start(kv8_append_kernel<4, kMany>);
+      case 8: return start(kv8_append_kernel<8, kMany>);
+      case 16: return start(kv8_append_kernel<16, kMany>);
+      default: return cudaErrorInvalidConfiguration;
+    }
+  };
+  return many ? launch(std::true_type()) : launch(std::false_type());
 }
 
 cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads, float scale, const Kv8Cache& cache,
