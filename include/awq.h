@@ -308,7 +308,8 @@ awq_status awq_silu_mul_fp8(const void* gate_up, void* x8, void* sx, int64_t M, 
  * written and read as zeros; nothing outside the buffers is touched.
  * Limits (AWQ_ERR_UNSUPPORTED): rows <= 2^24, seqs <= 2^20, seqs * heads <=
  * 2^24, q_heads <= 4096, rows * q_heads < 2^31, blocks * heads * block_tokens
- * < 2^31, table_width * block_tokens <= 2^28. rows = 0 or seqs = 0 is a no-op.
+ * < 2^31, table_width * block_tokens <= 2^28, |scale| <= 2^32. rows = 0 or
+ * seqs = 0 is a no-op.
  * q, k and v may be column ranges of one matrix: row r starts at element r *
  * stride, where the stride is a multiple of 8 and at least the row's width;
  * the heads of a row are contiguous. */
@@ -354,12 +355,14 @@ awq_status awq_kv8_append(const void* k, int64_t k_stride, const void* v, int64_
  * [rows][q_heads * head_dim]; query head i reads kv head i / (q_heads /
  * heads). The row at position p gives
  *   y = sum_{j <= p} softmax_j(scale * q . k_j) v_j,
- * and zeros when it sees no key (NaN when q is not finite). Made for the generation stage: one or a few
- * new tokens per sequence. More are right too, but every 16 rows of a kv head
- * read the sequence's keys anew. fp32 sums, the softmax weights rounded to
- * fp16 for their product with v. Work is split along the keys as well; parts
- * are added in a fixed order, so results are deterministic for a given device
- * and batch. A NaN code gives NaN in the rows that see it.
+ * and zeros when it sees no key (NaN when it sees some and q is not finite).
+ * Made for the generation stage: one or a few new tokens per sequence. More are
+ * right too, but every 16 rows of a kv head read the sequence's keys anew. Scores
+ * and sums are fp32, so a weight is off by about |scale q . k| 2^-23 of itself;
+ * weights are rounded to fp16 for their product with v (their sum is of the
+ * unrounded ones), to 2^-37 of the row's largest weight * 2^v_exp at the least.
+ * Work is split along the keys as well; parts are added in a fixed order, so
+ * results are deterministic for a given device and batch. A NaN code gives NaN in the rows that see it.
  * Source: TinyChat README (attention over the KV cache in the generation
  * stage); the 8-bit form is ours. */
 awq_status awq_kv8_attention(const void* q, int64_t q_stride, int q_heads, float scale, const awq_kv8_cache* cache,

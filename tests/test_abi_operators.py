@@ -195,3 +195,11 @@ def test_valid_arguments_without_a_device_stop_at_the_device_check():
     assert _append() == awq.AWQ_ERR_UNSUPPORTED
     assert _append(k=F, v=F + 2048, k_stride=6144, v_stride=6144) == awq.AWQ_ERR_UNSUPPORTED   # ranges of one matrix
     assert _attend() == awq.AWQ_ERR_UNSUPPORTED
+
+
+def test_kv8_attention_refuses_scales_beyond_its_scores():
+    # above 2^32 a row whose scores are all large and negative would count as one without keys
+    for s in (2.0 ** 32 * 1.001, -(2.0 ** 33), 1e30, -1e38):
+        assert _attend(scale=s) == awq.AWQ_ERR_UNSUPPORTED
+    for s in (2.0 ** 32, -(2.0 ** 32), 0.0):
+        assert _attend(scale=s, y=None) == awq.AWQ_ERR_INVALID_ARG       # gets past the scale

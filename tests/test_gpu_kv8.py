@@ -627,3 +627,22 @@ def test_append_grows_with_the_sequences_and_not_their_square():
             best = min(best, t0.elapsed_time(t1))
         times.append(best)
     assert times[1] < 24 * times[0], times           # 8 times the sequences: 8, where the square would be 64
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_largest_scores(D, sign):
+    # the largest q, codes, exponents and scale: every key of a row has the same
+    # score of about 2^95, whose fp32 steps are far above 1, so which keys count is
+    # open; y is a mean of some of them, not NaN
+    bt = Batch([1, 2], [700, 1300], 8, 2, D, 64, seed=31)
+    bt.q = torch.full_like(bt.q, 65504.0)
+    bt.cache.k.fill_(0x7E)
+    bt.cache.k_exp.fill_(31)
+    y = bt.attend(scale=sign * 2.0 ** 32).double().unflatten(1, (2, 4, D))
+    assert bt.status() == awq.AWQ_OK
+    for b in range(2):
+        v = bt.kept(b, "v")[0]
+        slack = 2.0 ** -10 * v.abs().amax(dim=0)[:, None]      # the weights' rounding and y's
+        r = y[bt.starts_h[b]:bt.starts_h[b + 1]]
+        assert (r <= v.amax(dim=0)[:, None] + slack).all() and (r >= v.amin(dim=0)[:, None] - slack).all()

@@ -1,6 +1,7 @@
 // C ABI entry points of libawq_b200.so (declared in include/awq.h): argument
 // checks, workspace layout, dispatch between the GEMV and GEMM paths.
 #include <cfloat>
+#include <cmath>
 #include <mutex>
 
 #include "awq_internal.cuh"
@@ -233,6 +234,9 @@ awq_status silu_impl(const void* gate_up, void* y, void* x8, void* sx, bool fp8,
 }
 
 constexpr int kMaxHeads = 4096;
+// |q . k| <= 128 * 65504 * 448 * 2^31 < 2^63: with it no score comes near 2^99,
+// below which the attention kernel takes a row's keys for none.
+constexpr float kMaxScale = 0x1p32f;
 
 awq_status check_kv8_sizes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t head_dim) {
   if (rows < 0 || seqs < 0 || q_heads <= 0 || heads <= 0 || q_heads % heads != 0) return AWQ_ERR_SHAPE;
@@ -532,6 +536,7 @@ awq_status awq_kv8_attention(const void* q, int64_t q_stride, int q_heads, float
   const int64_t width = (int64_t)q_heads * c.head_dim;
   if (q_stride < width || q_stride % 8 != 0) return AWQ_ERR_SHAPE;
   if (!(scale >= -FLT_MAX && scale <= FLT_MAX)) return AWQ_ERR_INVALID_ARG;
+  if (fabsf(scale) > kMaxScale) return AWQ_ERR_UNSUPPORTED;
   if (!q || !y) return AWQ_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(y)) return AWQ_ERR_ALIGNMENT;
   const size_t ybytes = (size_t)b.rows * width * 2, qbytes = row_bytes(b.rows, q_stride, width);

@@ -362,7 +362,7 @@ constexpr int kGroupCost = 2;
 // split, 32 sequences of 256 to 512 tokens 10.8 against 12.7 us, and a launch less
 // to wait for (but 256 sequences of 20 to 400: 37.5 against 34.9 us).
 constexpr int kWholeKeys = 512;
-constexpr float kNoM = -1e30f;  // M of a row that has seen no key: far below any x, finite
+constexpr float kNoM = -1e30f;  // M of a row that has seen no key: finite, far below any x (|x| < 2^96 by the limit of scale)
 
 // The group of units that starts in a CTA's range and ends in a later one's.
 struct Kv8Fix {
