@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
     }
     const Seq s = load_seq(bt, p.b, status);
     const int past = s.len - s.tokens;  // position of the first new row (rows at negative positions have no place)
-    const int j = min((max(past, 0) >> shift) + (int)(u - p.base), bt.table_width - 1);
+    const int j = (int)min((max(past, 0) >> shift) + (u - p.base), (int64_t)bt.table_width - 1);
     const int h = blockIdx.x;
     const int lo = max(max(past, 0) - j * bs, 0), hi = min(s.len - j * bs, bs);  // new rows of the block
     const int pieces = D / 8, rows_per_pass = kThreads / pieces;
