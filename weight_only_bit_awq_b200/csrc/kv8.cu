@@ -44,11 +44,15 @@ __device__ __forceinline__ Seq load_seq(const Kv8Batch& bt, int b, uint32_t* sta
 }
 
 // The items of all sequences, one after another: items(b) of them belong to
-// sequence b. Every thread of the CTA calls this; `total` is their sum, and
-// for item u (u < total) `b` its sequence and `base` the sequence's first.
+// sequence b. Every thread of the CTA calls this and counts a run of sequences;
+// returned is the sum, and whose run item u lies in is told by the counts alone: by
+// one thread's, even if the lists change before they are read again.
+struct Counted {
+  int64_t before, mine;  // items of the threads before this one, and this one's
+  __device__ __forceinline__ bool has(int64_t u) const { return u >= before && u < before + mine; }
+};
 template <typename Items>
-__device__ __forceinline__ int64_t total_items(int B, const Items& items, int64_t* scan /* [kWarps + 1] */,
-                                               int64_t& before) {
+__device__ __forceinline__ int64_t total_items(int B, const Items& items, int64_t* scan /* [kWarps] */, Counted& c) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (B + kThreads - 1) / kThreads;
   int64_t mine = 0;
@@ -62,10 +66,10 @@ __device__ __forceinline__ int64_t total_items(int B, const Items& items, int64_
   if (lane == 31) scan[warp] = inc;
   __syncthreads();
   int64_t total = 0;
-  before = inc - mine;
+  c = Counted{inc - mine, mine};
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += scan[w];
+    if (w < warp) c.before += scan[w];
     total += scan[w];
   }
   return total;
@@ -76,9 +80,10 @@ struct Place {
   int64_t base;
 };
 
-// Sequence of item u < total; `before` is this thread's from total_items, whose
-// caller has set *shared to the first sequence: what is found stays inside the
-// batch even if the lists change while a kernel reads them.
+// Sequence of item u < total, and the first of its items; `before` is this
+// thread's from total_items, whose caller has set *shared to the first sequence.
+// If the lists change while a kernel reads them, several threads or none may find
+// it: then b is still a sequence's and base at most u.
 template <typename Items>
 __device__ __forceinline__ Place find_item(int B, const Items& items, int64_t before, int64_t u, Place* shared) {
   const int per = (B + kThreads - 1) / kThreads;
@@ -192,13 +197,13 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
     return first < s.len && s.tokens > 0 ? ((s.len - 1) >> shift) - (first >> shift) + 1 : 0;
   };
   if (threadIdx.x == 0) place = Place{0, 0};
-  int64_t before;
-  const int64_t total = total_items(bt.seqs, items, scan, before);
+  Counted counted;
+  const int64_t total = total_items(bt.seqs, items, scan, counted);
   const int64_t ctas = (int64_t)gridDim.y * gridDim.z, cta = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
   auto first_item = [&](int64_t c) { return !kMany || total <= ctas ? c : total / ctas * c + total % ctas * c / ctas; };
   const int64_t u0 = first_item(cta), u1 = kMany ? min(first_item(cta + 1), total) : u0 + 1;
   if (u0 >= total) return;
-  Place p = find_item(bt.seqs, items, before, u0, &place);
+  Place p = find_item(bt.seqs, items, counted.before, u0, &place);
   // Every thread takes the same steps, whatever it reads in the lists.
   for (int64_t u = u0; u < u1; ++u) {
     if (kMany && u > u0) {
@@ -215,7 +220,9 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
     }
     const Seq s = load_seq(bt, p.b, status);
     const int past = s.len - s.tokens;  // position of the first new row (rows at negative positions have no place)
-    const int j = (int)min((max(past, 0) >> shift) + (u - p.base), (int64_t)bt.table_width - 1);
+    // (a grid of a CTA a block has fewer than 2^22 of them)
+    const int nth = kMany ? (int)min(u - p.base, (int64_t)bt.table_width) : (int)(u - p.base);
+    const int j = min((max(past, 0) >> shift) + nth, bt.table_width - 1);
     const int h = blockIdx.x;
     const int lo = max(max(past, 0) - j * bs, 0), hi = min(s.len - j * bs, bs);  // new rows of the block
     const int pieces = D / 8, rows_per_pass = kThreads / pieces;
@@ -475,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     return (int64_t)row_tiles(s) * group_units(s) * cache.heads;
   };
   if (tid == 0) walk.todo = ahead_valid[0] = 0;
-  int64_t before;
-  const int64_t total = total_items(bt.seqs, items, scan, before);
+  Counted counted;
+  const int64_t total = total_items(bt.seqs, items, scan, counted);
   const int64_t ctas = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
   if (tid == 0) a.fix[blockIdx.x].valid = 0;
   if ((int64_t)blockIdx.x >= ctas) return;
@@ -548,14 +555,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     walk = w;
     ahead_valid[slot] = found;
   };
-  {  // the thread that counted the sequence of the first unit begins
+  if (counted.has(u)) {  // the thread that counted the sequence of the first unit begins
     const int per = (bt.seqs + kThreads - 1) / kThreads;
-    int64_t at = before;
+    int64_t at = counted.before;
     for (int b = tid * per; b < min(bt.seqs, (tid + 1) * per); ++b) {
       const Seq s = load_seq(bt, b, status);
       const int tiles = row_tiles(s), units = group_units(s);
       const int64_t n = (int64_t)tiles * units * cache.heads;
-      if (u >= at && u < at + n) {
+      if (u < at + n) {
         const int64_t group_no = divide(u - at, units);
         Walk w;
         w.todo = u1 - u;
@@ -568,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
         w.per = units;
         walk = w;
         hand_out(0);
+        break;
       }
       at += n;
     }
