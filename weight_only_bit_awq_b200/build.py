@@ -16,8 +16,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libawq_b200.so")
 # The debug build (-DAWQ_DEBUG): every guarded global and shared access of the
-# pack, dequant, GEMV and GEMM kernels checks its index range first and records
-# AWQ_ERR_BOUNDS instead of faulting. Same entry points, separate file.
+# pack, dequant, GEMV, GEMM, norm, SiLU and cache kernels checks its index range
+# first and records AWQ_ERR_BOUNDS (where there is a status word) instead of
+# faulting. Same entry points, separate file.
 LIB_DEBUG = os.path.join(PKG, "libawq_b200_debug.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -33,6 +33,7 @@ struct Seq {
 
 // Sequence b, its bounds clamped to the buffers (a clamp is reported).
 __device__ __forceinline__ Seq load_seq(const Kv8Batch& bt, int b, uint32_t* status) {
+  if (!AWQ_CHECK(in_range(b, 1, bt.seqs), status)) return Seq{0, 0, 0};
   const int s0 = bt.starts[b], s1 = bt.starts[b + 1], len = bt.lens[b];
   const int cap = bt.table_width * bt.block_tokens;
   Seq s;
@@ -73,6 +74,16 @@ __device__ __forceinline__ int64_t total_items(int B, const Items& items, int64_
     total += scan[w];
   }
   return total;
+}
+
+// Codes of the cache's K (or V), for the debug build's checks.
+[[maybe_unused]] __device__ __forceinline__ int64_t code_bytes(const Kv8Cache& cache, const Kv8Batch& bt) {
+  return cache.blocks * cache.heads * bt.block_tokens * cache.head_dim;
+}
+// Entry j of sequence b's block table.
+__device__ __forceinline__ int table_block(const Kv8Batch& bt, int b, int j, uint32_t* status) {
+  const int64_t at = (int64_t)b * bt.table_width + j;
+  return AWQ_CHECK(in_range(at, 1, (int64_t)bt.seqs * bt.table_width), status) ? bt.table[at] : -1;
 }
 
 struct Place {
@@ -229,14 +240,14 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
     const int r0 = threadIdx.x / pieces, c = threadIdx.x % pieces;
     const int64_t row0 = (int64_t)s.row0 + (int64_t)j * bs - past;  // source row of the block's token 0
 
-    const int blk = bt.table[(int64_t)p.b * bt.table_width + j];
+    const int blk = table_block(bt, p.b, j, status);
     uint4 x[2][kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int r = r0 + i * rows_per_pass;
       const int64_t at = (int64_t)h * D + 8 * c;
       x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
-      if (r >= lo && r < hi) {
+      if (r >= lo && r < hi && AWQ_CHECK(in_range(row0 + r, 1, bt.rows), status)) {
         x[0][i] = *reinterpret_cast<const uint4*>(knew + (row0 + r) * k_stride + at);
         x[1][i] = *reinterpret_cast<const uint4*>(vnew + (row0 + r) * v_stride + at);
       }
@@ -275,7 +286,8 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
       const int e_old = lo > 0 ? usable(e_there[part]) : -128;
       const int e = max(needed_exponent(mag), e_old);
       if (threadIdx.x == 0) *exps[part] = (int8_t)e;
-      uint8_t* dst = (part ? cache.v : cache.k) + at * bs * D + 8 * c;
+      const int64_t dst_at = at * bs * D + 8 * c;
+      uint8_t* dst = (part ? cache.v : cache.k) + dst_at;
       const float inv = ldexpf(1.f, -e);
       if (!odd[part] && e >= -15 && e <= 14) {
         // 2^-e is an fp16 number, and a product that fp16 does not hold exactly
@@ -285,14 +297,16 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
         for (int i = 0; i < kIter; ++i) {
           const int r = r0 + i * rows_per_pass;
           const uint4& v = x[part][i];
-          if (r >= lo && r < hi)
+          if (r >= lo && r < hi && AWQ_CHECK(in_range(dst_at + r * D, 8, code_bytes(cache, bt)), status))
             *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(code2_h(v.x, inv2) | (code2_h(v.y, inv2) << 16),
                                                                 code2_h(v.z, inv2) | (code2_h(v.w, inv2) << 16));
         }
       } else {
 #pragma unroll 1
         for (int r = r0; r < hi; r += rows_per_pass) {
-          if (r < lo) continue;
+          if (r < lo || !AWQ_CHECK(in_range(row0 + r, 1, bt.rows) &&
+                                       in_range(dst_at + r * D, 8, code_bytes(cache, bt)), status))
+            continue;
           const __half* s = (part ? vnew + (row0 + r) * v_stride : knew + (row0 + r) * k_stride) + (int64_t)h * D + 8 * c;
           const uint4 v = *reinterpret_cast<const uint4*>(s);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -311,6 +325,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __half* __re
       if (e > e_old && lo > 0) {  // the codes that were there, under the larger exponent
         const float down = ldexpf(1.f, e_old - e);
         for (int r = r0; r < lo; r += rows_per_pass) {
+          if (!AWQ_CHECK(in_range(dst_at + r * D, 8, code_bytes(cache, bt)), status)) continue;
           uint2* old = reinterpret_cast<uint2*>(dst + r * D);
           const uint2 v = *old;
           const float2 a = h2f(lo_h2(v.x)), b = h2f(hi_h2(v.x)), d = h2f(lo_h2(v.y)), f = h2f(hi_h2(v.y));
@@ -382,7 +397,8 @@ struct AttnArgs {
   __half* out;
   int group;          // query heads per kv head
   float scale_log2;   // softmax scale times log2 e
-  float* partial;     // [ctas][2][slot]
+  float* partial;     // [ctas][2][slot], partial_floats in all
+  int64_t partial_floats;
   int slot;           // floats of a slot: rows * (D + 2)
   Kv8Fix* fix;        // [ctas]
   bool whole;         // groups are not split between CTAs
@@ -472,6 +488,10 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int bs = bt.block_tokens, shift = __ffs(bs) - 1;
+  // (debug build) whether bytes of shared memory lie in the ring
+  [[maybe_unused]] auto in_ring = [&](uint32_t at, int bytes) {
+    return AWQ_CHECK(in_range((int64_t)at - ptx::smem_u32(smem), bytes, L::kSmem - 128), status);
+  };
   auto row_tiles = [&](const Seq& s) { return (int)(((int64_t)s.tokens * a.group + L::kRows - 1) / L::kRows); };
   // a sequence with no keys still has one (empty) unit per row tile: its rows are zero
   auto key_tiles = [&](const Seq& s) { return max((s.len + kUnitKeys - 1) / kUnitKeys, 1); };
@@ -591,7 +611,9 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint2 v = make_uint2(0, 0);
-        if (r < sg.rows) v = *reinterpret_cast<const uint2*>(q + 16 * ks);
+        if (r < sg.rows &&
+            AWQ_CHECK(in_range(sg.row0 + r / a.group, 1, bt.rows) && in_range(sg.head, 1, cache.heads), status))
+          v = *reinterpret_cast<const uint2*>(q + 16 * ks);
         qf[nt][ks][0] = v.x;
         qf[nt][ks][1] = v.y;
       }
@@ -621,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
     blk = -1;
     k_exp = v_exp = 0;
     if (sub < steps * kSub && key < sg.seen) {
-      blk = bt.table[(int64_t)sg.b * bt.table_width + (key >> shift)];
+      blk = table_block(bt, sg.b, key >> shift, status);
       if (blk < 0 || blk >= cache.blocks) {
         record_status(status, AWQ_ERR_BOUNDS);
         blk = -1;
@@ -650,6 +672,9 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
 #pragma unroll
         for (int i = 0; i < 16 * D / 512; ++i) {
           const uint32_t to = (dst + sb * (16 * D) + i * 512) ^ (D == 128 ? (i & 1) << 6 : 0);
+          if (!AWQ_CHECK(in_range(at + i * 512, 16, code_bytes(cache, bt)), status) || !in_ring(to, 16) ||
+              !in_ring(to + L::kPartBytes, 16))
+            continue;
           copy16(to, cache.k + at + i * 512, bytes);
           copy16(to + L::kPartBytes, cache.v + at + i * 512, bytes);
         }
@@ -708,7 +733,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
 #pragma unroll
         for (int sb = 0; sb < kSub; ++sb) {
           uint32_t w[4];  // tokens g and g + 8 of piece ks, then of ks + 1
-          ldsm4((src + sb * (16 * D)) ^ (ks << 4), w);
+          const uint32_t from = (src + sb * (16 * D)) ^ (ks << 4);
+          ldsm4(in_ring(from, 16) ? from : ring, w);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t k0 = lo_h2(w[2 * i]), k1 = lo_h2(w[2 * i + 1]), k2 = hi_h2(w[2 * i]), k3 = hi_h2(w[2 * i + 1]);
@@ -813,7 +839,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
 #pragma unroll
           for (int i = 0; i < MT; i += 2) {
             uint32_t w[4];  // channels 2g, 2g + 1 of piece i: tokens 2t, 2t + 1, then + 8; the same of piece i + 1
-            ldsm4_trans((src + L::kPartBytes + sb * (16 * D)) ^ (i << 4), w);
+            const uint32_t from = (src + L::kPartBytes + sb * (16 * D)) ^ (i << 4);
+            ldsm4_trans(in_ring(from, 16) ? from : ring, w);
             if constexpr (decltype(careful)::value) {
               uint32_t nan[4], any = 0;
 #pragma unroll
@@ -885,11 +912,13 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
       const int r = lane_row(c);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
+        const int col = kWide ? (16 * i + 4 * t) ^ ((r & 1) << 4) : (16 * i + 2 * g) ^ ((t & 1) << 4);
+        if (!in_ring(ptx::smem_u32(mine + r * D + col), kWide ? 16 : 8)) continue;
         if constexpr (kWide)
-          *reinterpret_cast<float4*>(mine + r * D + ((16 * i + 4 * t) ^ ((r & 1) << 4))) =
+          *reinterpret_cast<float4*>(mine + r * D + col) =
               make_float4(o[i][0][2 * c], o[i][NT - 1][2 * c], o[i][0][2 * c + 1], o[i][NT - 1][2 * c + 1]);
         else
-          *reinterpret_cast<float2*>(mine + r * D + ((16 * i + 2 * g) ^ ((t & 1) << 4))) = make_float2(o[i][0][c], o[i][0][c + 2]);
+          *reinterpret_cast<float2*>(mine + r * D + col) = make_float2(o[i][0][c], o[i][0][c + 2]);
       }
       if ((kWide ? t : g) == 0) ml[warp][r] = make_float2(M[c], l[c]);
     }
@@ -908,7 +937,9 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
       for (int j = 0; j < kWarps; ++j) {
         const float2 v = ml[j][r];
         const float f = ex2(v.x - mx);
-        const float4 ow = *reinterpret_cast<const float4*>(parts[j] + r * D + (d ^ ((kWide ? r & 1 : r >> 1 & 1) << 4)));
+        const float* part = parts[j] + r * D + (d ^ ((kWide ? r & 1 : r >> 1 & 1) << 4));
+        if (!in_ring(ptx::smem_u32(part), 16)) continue;
+        const float4 ow = *reinterpret_cast<const float4*>(part);
         sum.x = fmaf(f, ow.x, sum.x), sum.y = fmaf(f, ow.y, sum.y);
         sum.z = fmaf(f, ow.z, sum.z), sum.w = fmaf(f, ow.w, sum.w);
         den = fmaf(f, v.y, den);
@@ -918,8 +949,10 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
         // a row that sees no key is zero; one whose scores are all -infinity is 0 / 0
         const float inv = min(w.past + token + 1, w.len) > 0 ? 1.f / den : 0.f;
         const int64_t at = (int64_t)(w.row0 + token) * cache.heads * a.group + (int64_t)w.head * a.group + (w.r0 + r) % a.group;
-        *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(f2h(sum.x * inv, sum.y * inv), f2h(sum.z * inv, sum.w * inv));
-      } else {
+        if (AWQ_CHECK(in_range(at, 1, (int64_t)bt.rows * cache.heads * a.group), status))
+          *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(f2h(sum.x * inv, sum.y * inv), f2h(sum.z * inv, sum.w * inv));
+      } else if (AWQ_CHECK(in_range(slot - a.partial, a.slot, a.partial_floats) &&
+                               in_range(r * D + d, 4, L::kRows * D), status)) {
         *reinterpret_cast<float4*>(slot + r * D + d) = sum;
         if (d == 0) *reinterpret_cast<float2*>(slot + L::kRows * D + 2 * r) = make_float2(mx, den);
       }
@@ -942,7 +975,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NT, ST>::kCtasPerSm)
 // of the first fixup CTAs to end are spread unevenly over the SMs (48 ragged
 // sequences with four CTAs per SM: 101 against 76 us).
 template <int D, bool kSplit>
-__global__ void __launch_bounds__(kThreads) kv8_fixup_kernel(const AttnArgs a, int heads, int tile_rows) {
+__global__ void __launch_bounds__(kThreads) kv8_fixup_kernel(const AttnArgs a, int heads, int rows, int tile_rows,
+                                                             uint32_t* status) {
   __shared__ float2 wml[kWarps];
   __shared__ float wsum[kWarps][D];
   ptx::griddep_wait();
@@ -951,6 +985,10 @@ __global__ void __launch_bounds__(kThreads) kv8_fixup_kernel(const AttnArgs a, i
   const int r = kSplit ? (int)blockIdx.y : (int)blockIdx.y * kWarps + warp;
   if (!f.valid || f.tile0 + r >= f.rows) return;
   const int parts = f.last_cta - (int)blockIdx.x + 1;
+  if (!AWQ_CHECK(in_range(2 * (int64_t)blockIdx.x * a.slot, (2 * (int64_t)parts - 1) * a.slot, a.partial_floats) &&
+                     in_range(tile_rows * D + 2 * r, 2, a.slot) && in_range(f.head, 1, heads) &&
+                     in_range((f.tile0 + r) / a.group + (int64_t)f.row0, 1, rows), status))
+    return;
   constexpr int E = D / 32;  // channels per lane
   auto part = [&](int i) { return a.partial + (((int64_t)blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * a.slot; };
   const int first = kSplit ? warp : 0, by = kSplit ? kWarps : 1;
@@ -1039,9 +1077,9 @@ cudaError_t launch_attention(AttnArgs a, const Kv8Cache& cache, const Kv8Batch& 
   // groups of units at most; with eight or more parts each, a CTA per row
   const int64_t groups = (int64_t)cache.heads * (bt.seqs + (int64_t)bt.rows * a.group / L::kRows);
   if (groups * 8 <= ctas)
-    return launch_pdl(kv8_fixup_kernel<D, true>, dim3((unsigned)ctas, L::kRows), kThreads, 0, stream, a, cache.heads, L::kRows);
-  return launch_pdl(kv8_fixup_kernel<D, false>, dim3((unsigned)ctas, L::kRows / kWarps), kThreads, 0, stream, a, cache.heads,
-                    L::kRows);
+    return launch_pdl(kv8_fixup_kernel<D, true>, dim3((unsigned)ctas, L::kRows), kThreads, 0, stream, a, cache.heads, bt.rows, L::kRows, status);
+  return launch_pdl(kv8_fixup_kernel<D, false>, dim3((unsigned)ctas, L::kRows / kWarps), kThreads, 0, stream, a, cache.heads, bt.rows,
+                    L::kRows, status);
 }
 
 }  // namespace
@@ -1092,6 +1130,7 @@ cudaError_t launch_kv8_attention(const __half* q, int64_t q_stride, int q_heads,
             ((int64_t)bt.seqs + bt.rows) * cache.heads <= 8 * device_info().sm_count;
   a.fix = reinterpret_cast<Kv8Fix*>(ws + kWsHeaderBytes);
   a.partial = reinterpret_cast<float*>(ws + kWsHeaderBytes + ctas * sizeof(Kv8Fix));
+  a.partial_floats = (int64_t)ctas * 2 * kMaxRows * (cache.head_dim + 2);
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
   // rows that share a kv head, by the mean of new tokens a sequence (lengths are on the device)
   const int64_t rows = ((int64_t)bt.rows + bt.seqs - 1) / bt.seqs * a.group;

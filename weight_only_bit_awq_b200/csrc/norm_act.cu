@@ -94,6 +94,17 @@ __device__ __forceinline__ void block_reduce(float& s, uint32_t& m, uint2* red, 
   warp_reduce();
 }
 
+// Vector c of the n of a row, and of the `all` of the matrix at `at`. (Here is no
+// status word: the debug build's checks skip the access, and so leave a wrong
+// output in place of a fault.)
+__device__ __forceinline__ bool inside(int c, int n, [[maybe_unused]] int64_t at, [[maybe_unused]] int64_t all) {
+  return c < n && AWQ_CHECK(in_range(at, 1, all), nullptr);
+}
+// Vector i of the dynamic shared memory.
+__device__ __forceinline__ bool in_ahead([[maybe_unused]] int i) {
+  return AWQ_CHECK(in_range(16 * (int64_t)i, 16, dynamic_smem_bytes()), nullptr);
+}
+
 struct NormArgs {
   const __half *x, *residual, *w;
   __half *h, *y;
@@ -141,7 +152,7 @@ __global__ void __launch_bounds__(kWide ? 1024 : 512, V <= 2 ? 2 : 1) rmsnorm_ke
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * NT + tid;
-      if (c >= a.K8) continue;
+      if (!inside(c, a.K8, row * a.K8 + c, a.M * a.K8) || !in_ahead((kIn * i + kIn - 1) * NT + tid)) continue;
       ptx::cp_async_16(ptx::smem_u32(ahead + kIn * i * NT + tid), x + row * a.K8 + c);
       if (kRes) ptx::cp_async_16(ptx::smem_u32(ahead + (kIn * i + 1) * NT + tid), residual + row * a.K8 + c);
     }
@@ -156,8 +167,9 @@ __global__ void __launch_bounds__(kWide ? 1024 : 512, V <= 2 ? 2 : 1) rmsnorm_ke
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * NT + tid;
-      vx[i] = c >= a.K8 ? zero : kAhead ? ahead[kIn * i * NT + tid] : x[base + c];
-      if (kRes) vr[i] = c >= a.K8 ? zero : kAhead ? ahead[(kIn * i + 1) * NT + tid] : residual[base + c];
+      const bool live = inside(c, a.K8, base + c, a.M * a.K8) && (!kAhead || in_ahead((kIn * i + kIn - 1) * NT + tid));
+      vx[i] = !live ? zero : kAhead ? ahead[kIn * i * NT + tid] : x[base + c];
+      if (kRes) vr[i] = !live ? zero : kAhead ? ahead[(kIn * i + 1) * NT + tid] : residual[base + c];
     }
     if (kAhead) copy(row + gridDim.x);
     float h[V][8], sum = 0.f, most = 0.f;
@@ -170,7 +182,7 @@ __global__ void __launch_bounds__(kWide ? 1024 : 512, V <= 2 ? 2 : 1) rmsnorm_ke
         unpack8(vr[i], r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] += r[j];
-        if (c < a.K8) reinterpret_cast<uint4*>(a.h)[base + c] = pack8(h[i]);
+        if (inside(c, a.K8, base + c, a.M * a.K8)) reinterpret_cast<uint4*>(a.h)[base + c] = pack8(h[i]);
       }
       float wf[8];
       if (kFp8) unpack8(c < a.K8 ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : zero, wf);
@@ -189,7 +201,7 @@ __global__ void __launch_bounds__(kWide ? 1024 : 512, V <= 2 ? 2 : 1) rmsnorm_ke
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * NT + tid;
-      if (c >= a.K8) continue;
+      if (!inside(c, a.K8, base + c, a.M * a.K8)) continue;
       if (kFp8) {
         reinterpret_cast<uint2*>(a.x8)[base + c] = codes8(h[i], f);
       } else {
@@ -216,7 +228,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
     const int64_t base = row * a.K8;
     float h[8], r[8], wf[8], sum = 0.f;
     uint32_t mx = 0;
-    for (int c = threadIdx.x; c < a.K8; c += blockDim.x) {
+    for (int c = threadIdx.x; inside(c, a.K8, base + c, a.M * a.K8); c += blockDim.x) {
       unpack8(reinterpret_cast<const uint4*>(a.x)[base + c], h);
       if (kRes) unpack8(reinterpret_cast<const uint4*>(a.residual)[base + c], r);
       unpack8(reinterpret_cast<const uint4*>(a.w)[c], wf);
@@ -229,7 +241,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormArgs a) {
     }
     block_reduce<true, kFp8>(sum, mx, red, parity);
     const float f = norm_factor<kFp8>(a, row, sum, mx);
-    for (int c = threadIdx.x; c < a.K8; c += blockDim.x) {
+    for (int c = threadIdx.x; inside(c, a.K8, base + c, a.M * a.K8); c += blockDim.x) {
       unpack8(reinterpret_cast<const uint4*>(a.x)[base + c], h);
       if (kRes) {
         unpack8(reinterpret_cast<const uint4*>(a.residual)[base + c], r);
@@ -282,12 +294,12 @@ __global__ void __launch_bounds__(256) silu_mul_kernel(const SiluArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = c0 + i * blockDim.x;
-    if (c < a.F8) vg[i] = g[c], vu[i] = g[a.F8 + c];
+    if (inside(c, a.F8, row * 2 * a.F8 + a.F8 + c, a.M * 2 * a.F8)) vg[i] = g[c], vu[i] = g[a.F8 + c];
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = c0 + i * blockDim.x;
-    if (c >= a.F8) break;
+    if (!inside(c, a.F8, row * a.F8 + c, a.M * a.F8)) break;
     float y[8];
     silu8(vg[i], vu[i], y);
     reinterpret_cast<uint4*>(a.y)[row * a.F8 + c] = pack8(y);
@@ -319,7 +331,7 @@ __global__ void __launch_bounds__(1024) silu_mul_fp8_kernel(const SiluArgs a) {
   auto copy = [&](int64_t row, int i) {
     const int c = i * NT + tid;
     const uint4* g = reinterpret_cast<const uint4*>(a.gu) + row * 2 * a.F8;
-    if (row < a.M && c < a.F8) {
+    if (row < a.M && inside(c, a.F8, row * 2 * a.F8 + a.F8 + c, a.M * 2 * a.F8) && in_ahead((2 * i + 1) * NT + tid)) {
       ptx::cp_async_16(ptx::smem_u32(ahead + 2 * i * NT + tid), g + c);
       ptx::cp_async_16(ptx::smem_u32(ahead + (2 * i + 1) * NT + tid), g + a.F8 + c);
     }
@@ -340,14 +352,15 @@ __global__ void __launch_bounds__(1024) silu_mul_fp8_kernel(const SiluArgs a) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = i * NT + tid;
-        vg[i] = c < a.F8 ? g[c] : make_uint4(0, 0, 0, 0);
-        vu[i] = c < a.F8 ? g[a.F8 + c] : make_uint4(0, 0, 0, 0);
+        const bool live = inside(c, a.F8, row * 2 * a.F8 + a.F8 + c, a.M * 2 * a.F8);
+        vg[i] = live ? g[c] : make_uint4(0, 0, 0, 0);
+        vu[i] = live ? g[a.F8 + c] : make_uint4(0, 0, 0, 0);
       }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (kAhead) {
-        const bool live = i * NT + tid < a.F8;
+        const bool live = i * NT + tid < a.F8 && in_ahead((2 * i + 1) * NT + tid);
         vg[i] = live ? ahead[2 * i * NT + tid] : make_uint4(0, 0, 0, 0);
         vu[i] = live ? ahead[(2 * i + 1) * NT + tid] : make_uint4(0, 0, 0, 0);
         copy(row + gridDim.x, i);
@@ -361,7 +374,7 @@ __global__ void __launch_bounds__(1024) silu_mul_fp8_kernel(const SiluArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = i * NT + tid;
-      if (c < a.F8) reinterpret_cast<uint2*>(a.x8)[row * a.F8 + c] = codes8(y[i], f);
+      if (inside(c, a.F8, row * a.F8 + c, a.M * a.F8)) reinterpret_cast<uint2*>(a.x8)[row * a.F8 + c] = codes8(y[i], f);
     }
   }
 }
@@ -376,14 +389,14 @@ __global__ void __launch_bounds__(1024) silu_mul_fp8_long_kernel(const SiluArgs 
     const uint4* g = reinterpret_cast<const uint4*>(a.gu) + row * 2 * a.F8;
     float y[8], none = 0.f;
     uint32_t mx = 0;
-    for (int c = threadIdx.x; c < a.F8; c += blockDim.x) {
+    for (int c = threadIdx.x; inside(c, a.F8, row * 2 * a.F8 + a.F8 + c, a.M * 2 * a.F8); c += blockDim.x) {
       silu8(g[c], g[a.F8 + c], y);
 #pragma unroll
       for (int j = 0; j < 8; ++j) mx = max(mx, mag(y[j]));
     }
     block_reduce<false, true>(none, mx, red, parity);
     const float f = silu_factor(a, row, mx);
-    for (int c = threadIdx.x; c < a.F8; c += blockDim.x) {
+    for (int c = threadIdx.x; inside(c, a.F8, row * 2 * a.F8 + a.F8 + c, a.M * 2 * a.F8); c += blockDim.x) {
       silu8(g[c], g[a.F8 + c], y);
       reinterpret_cast<uint2*>(a.x8)[row * a.F8 + c] = codes8(y, f);
     }
