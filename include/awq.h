@@ -248,7 +248,10 @@ awq_status awq_w4a8_gemm(const void* x8, const void* sx, const void* qweight, co
  * E4M3 form that awq_w4a8_gemm takes: sx[m] = max_k |y[m][k]| / 448 (fp32) and
  * x8[m][k] = e4m3(y[m][k] / sx[m]) (0 when sx[m] == 0). Inputs are fp16, all
  * arithmetic is fp32 and y is rounded once, to fp16 or to E4M3 (so the E4M3
- * form is not awq_fp8_quantize_x of the fp16 form, which rounds twice).
+ * form is not awq_fp8_quantize_x of the fp16 form, which rounds twice). y / sx is
+ * formed as a product with 448 / max|y|, and the SiLU's exponential and reciprocal
+ * are the special functions' (2^-22): where y / sx lies that near the middle of two
+ * codes, x8 may be the other one of e4m3 of the exact quotient.
  * Shapes: M >= 0 (0 is a no-op), K and F multiples of 8 (else AWQ_ERR_SHAPE),
  * K, F <= 2^22, M <= 2^24, M * F <= 2^40 (else AWQ_ERR_UNSUPPORTED). Every
  * pointer is 16-byte aligned. Outputs may not overlap inputs or one another
@@ -342,8 +345,10 @@ size_t awq_kv8_workspace_bytes(int64_t rows, int64_t seqs, int q_heads, int head
  * sequence already; then their codes are rewritten under the new exponent
  * (rounded once more only where a code becomes an E4M3 subnormal). New codes
  * are e4m3(value / 2^exp), round to nearest even; an infinity or a NaN becomes
- * the NaN code. Places behind a sequence's end keep their contents. A block
- * that gets new tokens must belong to one sequence only (full blocks may be
+ * the NaN code. Places behind a sequence's end keep their contents. An exponent
+ * only grows while a block holds tokens: if lens goes back (drafted tokens are
+ * rejected), it stays where they raised it, and so does what the older codes lost,
+ * until the block is filled from its first place again. A block that gets new tokens must belong to one sequence only (full blocks may be
  * shared). Calling it again with the same arguments leaves the cache as it is.
  * Source: TinyChat README (pre-allocated KV cache); the 8-bit form is ours. */
 awq_status awq_kv8_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,

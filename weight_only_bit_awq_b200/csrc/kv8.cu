@@ -379,10 +379,11 @@ constexpr float kPOffset = 12.f, kPMost = 15.f;
 // heads 51.4 and 40.0; three change them by less than 1 %).
 constexpr int kGroupCost = 2;
 // Where the block table holds no more keys than this, and the groups are not
-// many times the CTAs, a CTA takes whole groups and there is no fixup kernel: one
-// sequence of 128 / 512 / 1024 tokens 5.4 / 8.2 / 11.8 us against 7.0 / 7.6 / 7.9
-// split, 32 sequences of 256 to 512 tokens 10.8 against 12.7 us, and a launch less
-// to wait for (but 256 sequences of 20 to 400: 37.5 against 34.9 us).
+// many times the CTAs, a CTA takes whole groups and there is no fixup kernel, so a
+// launch less. In a graph, 8 kv heads, all of 128 / 256 / 512 tokens: one sequence 5.4 /
+// 6.2 / 7.3 us against 7.1 / 7.6 / 7.8 split, 32 sequences 6.7 / 7.9 / 10.5 against 8.2 /
+// 10.6 / 13.1 (but four of 512: 9.2 against 8.6, and one of 1024 11.8 against 8.0; 256
+// sequences of 20 to 400: 37.5 against 34.9); a call from Python 10.8 us against 13.1.
 constexpr int kWholeKeys = 512;
 constexpr float kNoM = -1e30f;  // M of a row that has seen no key: finite, far below any x (|x| < 2^96 by the limit of scale)
 
