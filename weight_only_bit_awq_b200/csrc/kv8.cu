@@ -184,9 +184,10 @@ __device__ __forceinline__ int usable(int e) { return max(min(e, 31), -32); }
 // most of the work and grows with their square, so there (kMany) as many CTAs as
 // about fit at once take equal ranges of blocks, find the first and count on from
 // it. Single tokens, 8 kv heads 128 wide, blocks of 64: 4096 sequences 2919 us with
-// a CTA a block and 202 so, 2048 399 and 89, 512 26.4 and 22.0, but 256 12.5 and
-// 13.1 (blocks of 16, 32 heads: 1024 206 and 100, 512 58.8 and 52.0, 256 25.2 and
-// 27.8). Two and eight CTAs an SM: 4096 sequences 270 and 245 us.
+// a CTA a block and 202 so, 2048 399 and 89, 1024 67 and 42 (blocks of 16, 32 heads:
+// 204 and 98), 1024 prompts of 64 tokens 135 and 87; but 512 prompts of 128 77 and 84,
+// 256 single tokens 12.5 and 13.1. Two and eight CTAs an SM: 4096 sequences 270 and
+// 245 us.
 constexpr int kManySeqs = 1024;
 constexpr int kManyCtasPerSm = 4;
 
